@@ -101,6 +101,9 @@ int nvfp4_abi_version(void);
  *                                          the prepacked weight's scale bytes not NaN, S_B finite;
  *                                          requantizing: bias finite, output S finite and > 0
  *   MX dequantize, MX GEMM                 E8M0 scale bytes not 0xFF
+ *   MX8 quantize, RMS norm, its backward   every floating input finite
+ *   W4A8 GEMM                              E4M3 codes not NaN, E8M0 scale bytes not 0xFF
+ *   rotary positions                       positions and frequencies finite
  * (unpack reads only bytes and is not scanned).  The wait makes every call synchronous.  A stream
  * under graph capture cannot be waited on, so captured calls skip the scans (a call on another
  * stream while a process-wide capture is running gets the runtime's refusal of its memset or
@@ -341,6 +344,112 @@ nvfp4_status_t nvfp4_mx_dequantize(const uint8_t *packed, const uint8_t *scales,
 nvfp4_status_t nvfp4_mx_gemm(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, const uint8_t *b_scales,
                              int64_t M, int64_t N, int64_t K, void *c, nvfp4_dtype_t c_dtype, int64_t ldc,
                              void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The 8-bit activation path: MXFP8 activations, the norm that writes them, their product with an
+ * MXFP4 weight, and the rotary positions of the queries and keys that come out of it.
+ *
+ * MXFP8 (the OCP microscaling definition, as for MXFP4 above): blocks of 32 consecutive values along
+ * K share one E8M0 scale byte b (X = 2^(b - 127)), X = 2^(floor(log2 amax) - 8) with b clamped to
+ * [0, 246] and b = 0 for an all-zero block; each value is the E4M3FN code nearest to v / X (ties to
+ * even, saturating at +-448).  codes are bytes [M][K], scales bytes [M][K/32], both dense.  A block
+ * that holds an infinity or a NaN gets b = 255 and zero codes (other blocks are not touched by it).
+ * K >= 32, K % 32 == 0.
+ *
+ * Pitches (ld_*) are elements from one row to the next; every fp32 or bf16 array is 16-byte
+ * aligned with a pitch of whole 16 bytes, except where a call says otherwise.  NVFP4_ERR_SHAPE also
+ * covers extents whose pitch times rows exceeds 2^40.
+ * ------------------------------------------------------------------------------------------- */
+
+/* MXFP8 of x [M][ld_x] (fp32 or bf16).  codes 16-byte aligned.  M == 0 is valid and touches nothing.
+   Bit-identical to the definition for every input. */
+nvfp4_status_t nvfp4_mx8_quantize(const void *x, nvfp4_dtype_t x_dtype, int64_t M, int64_t K, int64_t ld_x,
+                                  uint8_t *codes, uint8_t *scales, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition:
+ *     s = x + residual                        fp32 (s = x when residual is NULL)
+ *     h = s                                   rounded to dtype
+ *     inv_rms = 1 / sqrt(mean_k(s^2) + eps)   fp32, of the unrounded s
+ *     y = s * inv_rms * weight                (weight 1 when NULL)
+ *     codes, scales = MXFP8(y)                of the fp32 y
+ * One pass: x and residual are read once, and what is asked for is written once.
+ *
+ *   x, residual    [M][ld_x], [M][ld_residual] of dtype (fp32 or bf16); residual may be NULL.
+ *   K              32 .. 32768, K % 32 == 0.
+ *   weight         NULL, or [K] of weight_dtype (fp32 or bf16), 16-byte aligned.
+ *   eps            finite, > 0 (else NVFP4_ERR_MODE).
+ *   h              NULL, or [M][ld_h] of dtype.  May be x or residual itself (same pitch).
+ *   codes, scales  both or neither; codes 16-byte aligned.
+ *   y              NULL, or [M][ld_y] of y_dtype.  fake_quantize != 0: y receives the values that
+ *                  the MXFP8 codes stand for (quantization-aware training), else the norm itself.
+ *                  Of codes and y at least one is needed.
+ *   inv_rms        NULL, or fp32 [M] (the backward pass reads it).
+ *   M == 0 is valid and touches nothing.
+ * A row with a non-finite value makes that row's outputs non-finite (its blocks' scales 255).
+ *
+ * Backward, for the gradient dy of y (the straight-through estimator passes it through the
+ * quantization) and dh of h (NULL: none): with n = h inv_rms, g = dy weight,
+ *     dx = inv_rms (g - n mean_k(g n)) + dh   (the gradient of x and, the same, of residual)
+ *     dweight[k] = sum_m dy n                 fp32
+ *   dy, h, dh, dx  of dtype at their own pitches; dx may be dy or dh itself (same pitch).
+ *   dweight        NULL, or [K] fp32, 16-byte aligned; then workspace holds at least
+ *                  nvfp4_rmsnorm_backward_workspace_bytes(M, K) bytes, 16-byte aligned, with no
+ *                  initialization.  Sums run in a fixed order: equal inputs give equal bits.
+ *   M == 0 writes dweight = 0 and touches nothing else.
+ * ------------------------------------------------------------------------------------------- */
+nvfp4_status_t nvfp4_rmsnorm(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,
+                             nvfp4_dtype_t dtype, int64_t M, int64_t K, const void *weight,
+                             nvfp4_dtype_t weight_dtype, float eps, void *h, int64_t ld_h, uint8_t *codes,
+                             uint8_t *scales, void *y, nvfp4_dtype_t y_dtype, int64_t ld_y, int fake_quantize,
+                             float *inv_rms, void *stream);
+size_t nvfp4_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
+nvfp4_status_t nvfp4_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *h, int64_t ld_h, const void *dh,
+                                      int64_t ld_dh, nvfp4_dtype_t dtype, int64_t M, int64_t K, const void *weight,
+                                      nvfp4_dtype_t weight_dtype, const float *inv_rms, void *dx, int64_t ld_dx,
+                                      float *dweight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * W4A8 product: Y[M][N] = A B^T with A [M][K] MXFP8 (codes and scales as nvfp4_mx8_quantize and
+ * nvfp4_rmsnorm write them) and B [N][K] canonical MXFP4 (nvfp4_mx_quantize), for prompts and for
+ * single tokens.  Products are exact and accumulate in fp32; only the summation order differs from
+ * dequantize-then-matmul.  a, b 16-byte aligned, a_scales, b_scales 4-byte aligned; c as for
+ * nvfp4_gemm (fp32 or bf16, base 16-byte aligned, any ldc >= N).  K % 32 == 0; M, N, K < 2^30.
+ * M == 0 or N == 0 is valid and touches nothing.
+ * ------------------------------------------------------------------------------------------- */
+nvfp4_status_t nvfp4_mx_gemm_w4a8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b, const uint8_t *b_scales,
+                                  int64_t M, int64_t N, int64_t K, void *c, nvfp4_dtype_t c_dtype, int64_t ldc,
+                                  void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Rotary positions with several axes (time, height, width of images and video; one axis is the
+ * usual rotary position).  Of each head's D elements the first axis_dims[0] turn by the token's
+ * first coordinate, the next axis_dims[1] by the second, and so on; elements past the sections pass
+ * through unchanged.  Pair p (numbered through the sections) turns by
+ *     angle = RN32(positions[t][axis of p] * inv_freq[p]):  (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin)
+ * and with inverse != 0 by -angle, which is the gradient of the forward call (the rotation's
+ * transpose).  Sine and cosine are within 1e-6 of that angle's for |angle| < 2^24.
+ *
+ *   x            [T][H][D] of dtype (fp32 or bf16) at token pitch ld_token and head pitch ld_head
+ *                (elements, whole 16 bytes): the queries and keys inside a QKV linear's output are
+ *                one such tensor.
+ *   D            8 .. 1024, D % 8 == 0.   H <= 2^20, T < 2^31.
+ *   positions    device fp32 [T][n_axes], any finite values.      n_axes  1 .. 4.
+ *   axis_dims    HOST int32 [n_axes], each even and >= 0, their sum <= D.
+ *   inv_freq     device fp32, one per pair (sum of axis_dims / 2).
+ *   layout       NVFP4_ROPE_PAIRS: a pair is two neighbours (2 i, 2 i + 1 of the section);
+ *                NVFP4_ROPE_HALVES: elements i and i + axis_dim / 2 of the section.
+ *   y            as x, at its own pitches, rows not overlapping; may be x itself (same pitches), and
+ *                otherwise must not overlap it.
+ *   T == 0 or H == 0 is valid and touches nothing.
+ * ------------------------------------------------------------------------------------------- */
+typedef enum { NVFP4_ROPE_PAIRS = 0, NVFP4_ROPE_HALVES = 1, NVFP4_ROPE_MIN_ENUM_ = -0x7fffffff - 1,
+               NVFP4_ROPE_MAX_ENUM_ = 0x7fffffff } nvfp4_rope_layout_t;
+
+nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, int64_t H, int64_t D, int64_t ld_token,
+                               int64_t ld_head, const float *positions, int n_axes, const int32_t *axis_dims,
+                               const float *inv_freq, nvfp4_rope_layout_t layout, int inverse, void *y,
+                               int64_t ldy_token, int64_t ldy_head, void *stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from enum import IntEnum
+from typing import NamedTuple
 
 import torch
 
@@ -46,6 +47,8 @@ EXPORTED = (
     "nvfp4_unpack_weight_bs", "nvfp4_gemm_bs", "nvfp4_gemm_requant_bs",
     "nvfp4_mx_quantize", "nvfp4_mx_dequantize", "nvfp4_mx_gemm",
     "nvfp4_quantize_noalloc", "nvfp4_set_debug_checks",
+    "nvfp4_mx8_quantize", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes", "nvfp4_rmsnorm_backward",
+    "nvfp4_mx_gemm_w4a8", "nvfp4_rope_axes",
 )
 
 _lib = None
@@ -123,6 +126,21 @@ def lib():
     L.nvfp4_quantize_noalloc.restype = _i
     L.nvfp4_quantize_noalloc.argtypes = [_vp, _i, _i64, _i64, _i64, _i, _vp, _vp, _vp, _i, _vp]
     L.nvfp4_mx_gemm.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i, _i64, _vp]
+    L.nvfp4_mx8_quantize.restype = _i
+    L.nvfp4_mx8_quantize.argtypes = [_vp, _i, _i64, _i64, _i64, _vp, _vp, _vp]
+    L.nvfp4_rmsnorm.restype = _i
+    L.nvfp4_rmsnorm.argtypes = [_vp, _i64, _vp, _i64, _i, _i64, _i64, _vp, _i, ctypes.c_float, _vp, _i64, _vp, _vp,
+                                _vp, _i, _i64, _i, _vp, _vp]
+    L.nvfp4_rmsnorm_backward_workspace_bytes.restype = _sz
+    L.nvfp4_rmsnorm_backward_workspace_bytes.argtypes = [_i64, _i64]
+    L.nvfp4_rmsnorm_backward.restype = _i
+    L.nvfp4_rmsnorm_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i, _i64, _i64, _vp, _i, _vp, _vp, _i64,
+                                         _vp, _vp, _sz, _vp]
+    L.nvfp4_mx_gemm_w4a8.restype = _i
+    L.nvfp4_mx_gemm_w4a8.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i, _i64, _vp]
+    L.nvfp4_rope_axes.restype = _i
+    L.nvfp4_rope_axes.argtypes = [_vp, _i, _i64, _i64, _i64, _i64, _i64, _vp, _i, _vp, _vp, _i, _i, _vp, _i64, _i64,
+                                  _vp]
     _lib = L
     return L
 
@@ -432,6 +450,274 @@ def nvfp4_mx_gemm(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sc
     return out
 
 
+# ---- the 8-bit activation path: MXFP8, RMS norm, W4A8, rotary positions --------------------------
+
+ROPE_PAIRS, ROPE_HALVES = 0, 1
+
+
+def _same_device(ref: torch.Tensor, **tensors):
+    """Every given tensor lies on ref's device, which is the current one (the library launches there)."""
+    if not ref.is_cuda:
+        raise ValueError("the operands must be device tensors")
+    if ref.device.index != torch.cuda.current_device():
+        raise ValueError(f"the operands are on {ref.device}, which is not the current device")
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+
+
+def _on_stream(stream, *allocated):
+    """Raw handle of the stream to launch on; what this call allocated (on the current stream) is kept
+    from reuse until that stream is done with it."""
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    for t in allocated:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _dense(t: torch.Tensor, name: str, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _matrix(t: torch.Tensor, name: str, shape, dtype):
+    """Row pitch (elements) of a 2-D tensor of the given shape and type with unit stride along K."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along K")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def nvfp4_mx8_quantize(x: torch.Tensor, *, codes=None, scales=None, stream=None):
+    """MXFP8-quantize x [M, K] (fp32 or bf16, K % 32 == 0).  Returns (codes u8 [M, K], scales u8 [M, K/32]):
+    E4M3 codes (``codes.view(torch.float8_e4m3fn)`` reads them) under one E8M0 byte per 32 values."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    M, K = x.shape
+    ld = _matrix(x, "x", (M, K), x.dtype)
+    _same_device(x, codes=codes, scales=scales)
+    codes = torch.empty((M, K), dtype=torch.uint8, device=x.device) if codes is None else \
+        _dense(codes, "codes", (M, K), torch.uint8)
+    scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device) if scales is None else \
+        _dense(scales, "scales", (M, K // 32), torch.uint8)
+    st = lib().nvfp4_mx8_quantize(x.data_ptr(), _dtype_code(x.dtype), M, K, ld, codes.data_ptr(), scales.data_ptr(),
+                                  _on_stream(stream, codes, scales))
+    _check(st, "nvfp4_mx8_quantize")
+    return codes, scales
+
+
+class RMSNormOutput(NamedTuple):
+    """What nvfp4_rmsnorm wrote; None for what was not asked for."""
+    h: torch.Tensor | None
+    codes: torch.Tensor | None
+    scales: torch.Tensor | None
+    y: torch.Tensor | None
+    inv_rms: torch.Tensor | None
+
+
+def nvfp4_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                  eps: float = 1e-6, *, mx8: bool = True, y_dtype: torch.dtype | None = None,
+                  fake_quantize: bool = False, save_inv_rms: bool = False, h=None, stream=None) -> RMSNormOutput:
+    """y = rmsnorm(x + residual) * weight of [M, K] tensors (fp32 or bf16, K % 32 == 0, K <= 32768).
+
+    mx8: write y as MXFP8 (codes, scales), the activation of nvfp4_mx_gemm_w4a8.  y_dtype: also write y
+    itself (fp32 or bf16); with fake_quantize the values its MXFP8 codes stand for.  With a residual, h
+    is the sum, rounded to x's type (into the given h, which may be x or residual, or a new tensor);
+    without one it is written only into a given h.  save_inv_rms: keep what the backward pass needs."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    M, K = x.shape
+    dev = x.device
+    ld_x = _matrix(x, "x", (M, K), x.dtype)
+    ld_r = 0 if residual is None else _matrix(residual, "residual", (M, K), x.dtype)
+    _same_device(x, residual=residual, weight=weight, h=h)
+    if weight is not None:
+        _dense(weight, "weight", (K,), weight.dtype)
+    if fake_quantize and y_dtype is None:
+        raise ValueError("fake_quantize needs y_dtype")
+    new_h = None
+    if h is None and residual is not None:
+        h = new_h = torch.empty((M, K), dtype=x.dtype, device=dev)
+    ld_h = 0 if h is None else _matrix(h, "h", (M, K), x.dtype)
+    codes = scales = y = inv_rms = None
+    if mx8:
+        codes = torch.empty((M, K), dtype=torch.uint8, device=dev)
+        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
+    if y_dtype is not None:
+        y = torch.empty((M, K), dtype=y_dtype, device=dev)
+    if save_inv_rms:
+        inv_rms = torch.empty(M, dtype=torch.float32, device=dev)
+    st = lib().nvfp4_rmsnorm(x.data_ptr(), ld_x, _addr(residual), ld_r, _dtype_code(x.dtype), M, K, _addr(weight),
+                             0 if weight is None else _dtype_code(weight.dtype), eps, _addr(h), ld_h, _addr(codes),
+                             _addr(scales), _addr(y), 0 if y is None else _dtype_code(y_dtype), K,
+                             1 if fake_quantize else 0, _addr(inv_rms),
+                             _on_stream(stream, new_h, codes, scales, y, inv_rms))
+    _check(st, "nvfp4_rmsnorm")
+    return RMSNormOutput(h, codes, scales, y, inv_rms)
+
+
+def nvfp4_rmsnorm_backward_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().nvfp4_rmsnorm_backward_workspace_bytes(M, K))
+
+
+def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, inv_rms: torch.Tensor, weight: torch.Tensor | None = None,
+                           dh: torch.Tensor | None = None, *, dweight: bool = True, dx=None, workspace=None,
+                           stream=None):
+    """Gradients of nvfp4_rmsnorm from dy (gradient of y), the forward's h (x where there was no residual)
+    and inv_rms, and dh (gradient of h, or None).  Returns (dx, dw): dx [M, K] in h's type is the gradient
+    of x and of residual; dw fp32 [K] is weight's (None with dweight=False)."""
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D")
+    M, K = h.shape
+    dev = h.device
+    ld_h = _matrix(h, "h", (M, K), h.dtype)
+    ld_dy = _matrix(dy, "dy", (M, K), h.dtype)
+    ld_dh = 0 if dh is None else _matrix(dh, "dh", (M, K), h.dtype)
+    _dense(inv_rms, "inv_rms", (M,), torch.float32)
+    _same_device(h, dy=dy, dh=dh, inv_rms=inv_rms, weight=weight, dx=dx, workspace=workspace)
+    if weight is not None:
+        _dense(weight, "weight", (K,), weight.dtype)
+    if dx is None:
+        dx = torch.empty((M, K), dtype=h.dtype, device=dev)
+    ld_dx = _matrix(dx, "dx", (M, K), h.dtype)
+    dw = None
+    if dweight:
+        dw = torch.empty(K, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(nvfp4_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().nvfp4_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, _addr(dh), ld_dh, _dtype_code(h.dtype),
+                                      M, K, _addr(weight), 0 if weight is None else _dtype_code(weight.dtype),
+                                      inv_rms.data_ptr(), dx.data_ptr(), ld_dx, _addr(dw), _addr(workspace), ws_bytes,
+                                      _on_stream(stream, dx, dw, workspace))
+    _check(st, "nvfp4_rmsnorm_backward")
+    return dx, dw
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, fake_quantize):
+        ctx.set_materialize_grads(False)
+        x2 = _rows_of(x)
+        out = nvfp4_rmsnorm(x2, None if residual is None else _rows_of(residual), weight, eps, mx8=False,
+                            y_dtype=x.dtype, fake_quantize=fake_quantize, save_inv_rms=True)
+        ctx.save_for_backward(x2 if residual is None else out.h, out.inv_rms, weight)
+        ctx.shape = x.shape
+        ctx.has_residual = residual is not None
+        return out.y.view(x.shape), None if residual is None else out.h.view(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy, dh):
+        h, inv_rms, weight = ctx.saved_tensors
+        want_dw = weight is not None and ctx.needs_input_grad[2]
+        if dy is None:  # y is not used: only the sum's gradient goes through
+            return dh, dh if ctx.has_residual else None, torch.zeros_like(weight) if want_dw else None, None, None
+        dx, dw = nvfp4_rmsnorm_backward(_rows_of(dy), h, inv_rms, weight, None if dh is None else _rows_of(dh),
+                                        dweight=want_dw)
+        dx = dx.view(ctx.shape)
+        return dx, dx if ctx.has_residual else None, dw.to(weight.dtype) if want_dw else None, None, None
+
+
+def _rows_of(t: torch.Tensor) -> torch.Tensor:
+    """t [..., K] as a matrix of rows of K that the kernels take (copied only where its layout needs it)."""
+    m = t.reshape(-1, t.shape[-1])
+    es = t.element_size()
+    return m if m.stride(1) == 1 and m.stride(0) * es % 16 == 0 and m.data_ptr() % 16 == 0 else m.contiguous()
+
+
+def rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+            eps: float = 1e-6, fake_quantize: bool = False):
+    """Differentiable RMS norm with the residual's addition over the last dimension: (y, h) with h the sum
+    (None without a residual).  fake_quantize: y holds the values of its MXFP8 codes, with a
+    straight-through gradient (quantization-aware training)."""
+    return _RMSNorm.apply(x, residual, weight, eps, fake_quantize)
+
+
+def nvfp4_mx_gemm_w4a8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+                       out_dtype: torch.dtype = torch.bfloat16, *, out=None, stream=None) -> torch.Tensor:
+    """Y = A B^T with A [M, K] MXFP8 (codes u8 [M, K], scales u8 [M, K/32]) and B [N, K] MXFP4 (packed u8
+    [N, K/2], scales u8 [N, K/32]); all dense.  out: a tensor [M, N] (fp32 or bf16, unit stride along N)."""
+    M, K = a.shape
+    N = b.shape[0]
+    _dense(a, "a", (M, K), torch.uint8)
+    _dense(a_scales, "a_scales", (M, K // 32), torch.uint8)
+    _dense(b, "b", (N, K // 2), torch.uint8)
+    _dense(b_scales, "b_scales", (N, K // 32), torch.uint8)
+    _same_device(a, a_scales=a_scales, b=b, b_scales=b_scales, out=out)
+    new = None
+    if out is None:
+        out = new = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    ldc = _matrix(out, "out", (M, N), out.dtype)
+    st = lib().nvfp4_mx_gemm_w4a8(a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, N, K,
+                                  out.data_ptr(), _dtype_code(out.dtype), ldc, _on_stream(stream, new))
+    _check(st, "nvfp4_mx_gemm_w4a8")
+    return out
+
+
+def rope_inv_freq(axis_dims, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Frequencies of nvfp4_rope_axes: theta^(-2 i / d) for the pairs i of each axis' d elements, fp32."""
+    parts = [float(theta) ** (-torch.arange(0, d, 2, dtype=torch.float64) / d) for d in axis_dims if d > 0]
+    return torch.cat(parts).float().to(device) if parts else torch.empty(0, device=device)
+
+
+def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_freq: torch.Tensor, *,
+                    layout: int = ROPE_PAIRS, inverse: bool = False, out=None, stream=None) -> torch.Tensor:
+    """Rotary positions with several axes of x [T, H, D] (fp32 or bf16; token and head strides free, unit
+    stride along D).  positions fp32 [T, axes]; axis_dims: how many leading elements of a head each axis
+    turns; inv_freq fp32, one per pair (rope_inv_freq).  inverse: turn back (the gradient).  out: a
+    tensor [T, H, D], x itself to turn in place, or None for a new dense one."""
+    if x.dim() != 3:
+        raise ValueError("x must be [T, H, D]")
+    T, H, D = x.shape
+    dims = (ctypes.c_int32 * len(axis_dims))(*axis_dims)
+    _dense(positions, "positions", (T, len(axis_dims)), torch.float32)
+    _dense(inv_freq, "inv_freq", (sum(axis_dims) // 2,), torch.float32)
+    _same_device(x, positions=positions, inv_freq=inv_freq, out=out)
+    new = None
+    if out is None:
+        out = new = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    if x.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("x and out must have unit stride along D")
+    st = lib().nvfp4_rope_axes(x.data_ptr(), _dtype_code(x.dtype), T, H, D, x.stride(0), x.stride(1),
+                               positions.data_ptr(), len(axis_dims), dims, inv_freq.data_ptr(), layout,
+                               1 if inverse else 0, out.data_ptr(), out.stride(0), out.stride(1),
+                               _on_stream(stream, new))
+    _check(st, "nvfp4_rope_axes")
+    return out
+
+
+class _RopeAxes(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, positions, axis_dims, inv_freq, layout):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.how = (axis_dims, layout)
+        return nvfp4_rope_axes(x, positions, axis_dims, inv_freq, layout=layout)
+
+    @staticmethod
+    def backward(ctx, dy):
+        positions, inv_freq = ctx.saved_tensors
+        axis_dims, layout = ctx.how
+        dx = nvfp4_rope_axes(dy.contiguous(), positions, axis_dims, inv_freq, layout=layout, inverse=True)
+        return dx, None, None, None, None
+
+
+def rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_freq: torch.Tensor,
+              layout: int = ROPE_PAIRS) -> torch.Tensor:
+    """Differentiable nvfp4_rope_axes (the gradient of x is the inverse rotation)."""
+    return _RopeAxes.apply(x, positions, tuple(axis_dims), inv_freq, layout)
+
+
 __all__ = [
     "Status", "NVFP4Error", "lib", "LIB_PATH", "EXPORTED", "F32", "BF16", "W4A4", "W4A16",
     "SCALE_DYNAMIC", "SCALE_STATIC", "nvfp4_set_debug_checks",
@@ -442,4 +728,7 @@ __all__ = [
     "nvfp4_gemm_workspace_bytes", "nvfp4_gemm",
     "ACT_NONE", "ACT_GELU_TANH", "nvfp4_gemm_requant_workspace_bytes", "nvfp4_gemm_requant",
     "nvfp4_mx_quantize", "nvfp4_mx_dequantize", "nvfp4_mx_gemm",
+    "nvfp4_mx8_quantize", "RMSNormOutput", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes",
+    "nvfp4_rmsnorm_backward", "rmsnorm", "nvfp4_mx_gemm_w4a8",
+    "ROPE_PAIRS", "ROPE_HALVES", "rope_inv_freq", "nvfp4_rope_axes", "rope_axes",
 ]

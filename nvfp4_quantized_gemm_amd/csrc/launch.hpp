@@ -5,6 +5,8 @@
 
 #include <atomic>
 
+#include "common.hpp"
+
 namespace nvfp4 {
 
 // Per-device, per-kernel one-time setup of the dynamic LDS limit (kernels whose LDS exceeds the
@@ -123,5 +125,68 @@ hipError_t launch_mx_dequantize(const uint8_t *packed, const uint8_t *scales, in
                                 int out_dtype, int64_t ld_y, hipStream_t stream);
 hipError_t launch_mx_gemm(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs, int64_t M,
                           int64_t N, int64_t K, void *c, int out_dtype, int64_t ldc, hipStream_t stream);
+
+// ---- the 8-bit activation path ----------------------------------------------------------------------
+
+// dtype codes: 0 fp32, 1 bf16
+struct NormArgs {  // rmsnorm.hip; null pointers: input taken as absent, output not written
+  const void *x, *residual;
+  int dtype;
+  int64_t M, K, ld_x, ld_r;
+  const void *weight;
+  int w_dtype;
+  float eps, inv_k;
+  void *h;
+  int64_t ld_h;
+  uint8_t *codes, *scales;
+  void *y;
+  int y_dtype;
+  int64_t ld_y;
+  int fake;
+  float *inv_rms;
+};
+hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t stream);
+
+constexpr int64_t kNormMaxK = 32768;  // a row lives in one workgroup's registers
+struct NormGradArgs {
+  const void *dy, *h, *dh;
+  int dtype;
+  int64_t M, K, ld_dy, ld_h, ld_dh;
+  const void *weight;
+  int w_dtype;
+  const float *inv_rms;
+  float inv_k;
+  void *dx;
+  int64_t ld_dx;
+  float *partial;  // [norm_grad_rows(M, K)][K], or null where no dweight is wanted
+};
+int norm_grad_rows(int64_t M, int64_t K);
+hipError_t launch_rmsnorm_backward(const NormGradArgs &a, float *dweight, hipStream_t stream);
+
+constexpr int kRopeMaxAxes = 4;
+constexpr int64_t kRopeMaxD = 1024;
+struct RopeArgs {  // rope.hip
+  const void *x;
+  void *y;
+  int dtype;
+  int64_t T, ld_t, ld_h, ldy_t, ldy_h;
+  int H, D, n_axes, pairs, halves, inverse;
+  int pair_end[kRopeMaxAxes];  // pairs of the axes up to and with this one
+  const float *positions, *inv_freq;
+  int tokens = 0;  // per workgroup; the launcher sets this and the divisors
+  FastDiv div_c{}, div_h{};
+};
+hipError_t launch_rope(RopeArgs a, hipStream_t stream);
+
+hipError_t launch_mx8_quantize(const void *x, int dtype, int64_t M, int64_t K, int64_t ld, uint8_t *codes,
+                               uint8_t *scales, hipStream_t stream);
+struct W4A8Args {  // w4a8.hip
+  const uint8_t *a, *as, *b, *bs;
+  int64_t M, N, K;
+  void *c;
+  int out_dtype;
+  int64_t ldc;
+};
+hipError_t launch_w4a8(const W4A8Args &g, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -1,0 +1,309 @@
+// Root-mean-square norm with the residual's addition and MXFP8 output, and its backward pass (gfx950).
+//
+//   s = x + residual           (fp32)              h = s rounded to x's type
+//   inv_rms = 1 / sqrt(mean_k s^2 + eps)           y = s inv_rms weight
+//   codes, scales = MXFP8(y)                       (mx8.hpp)
+// The norm is of the fp32 sum, not of the rounded h: h is rounded once, for the next layer, and y
+// once, to its 8 bits.  Sums of squares and everything before the encoding are fp32.
+//
+// Backward, with n = h inv_rms, g = dy weight, c = mean_k(g n):
+//   dx = inv_rms (g - n c) + dh  (x's gradient and the residual's)      dweight = sum_m dy n
+#include "launch.hpp"
+#include "mx8.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v += swap_lane1(v);
+  v += swap_lane2(v);
+  v += swap_lane4(v);
+  v += swap_lane8(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// Sum over the TPR threads of a row; every one of them gets it.  TPR == 64: the row is one wave's
+// and no other wave is waited for.  Otherwise the row is the whole workgroup's, and `red` holds two
+// sets of partials used in turn, so one barrier per row is enough.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *red, int phase) {
+  v = wave_sum(v);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    float *r = red + (phase & 1) * W;
+    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += r[i];
+  }
+  return v;
+}
+
+// A weight vector: 1 where there is no weight, else 8 values of either type.
+__device__ __forceinline__ void load_weight(const void *w, int w_dtype, int64_t k, float (&v)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+  } else if (w_dtype == 0) {
+    Vec8<0> t;
+    t.load<false>(w, k);
+    t.get(v);
+  } else {
+    Vec8<1> t;
+    t.load<false>(w, k);
+    t.get(v);
+  }
+}
+
+}  // namespace
+
+// TPR threads (64, 256 or 1024) hold a row in registers, NV vectors of 8 elements each; workgroups
+// of 256 threads take 4 rows at TPR = 64.
+template <int DT, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
+  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+  __shared__ float red[TPR > 64 ? 2 * TPR / 64 : 1];
+  const int t = threadIdx.x % TPR;
+  const int nseg = (int)(a.K / 8);
+  int phase = 0;
+  for (int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; m < a.M; m += (int64_t)gridDim.x * kRows, ++phase) {
+    float s[NV][8];
+    float sq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int seg = j * TPR + t;
+      const bool in = seg < nseg;
+      Vec8<DT> x;
+      x.zero();
+      if (in) x.template load<true>(a.x, m * a.ld_x + 8 * seg);
+      x.get(s[j]);
+      if (a.residual) {
+        Vec8<DT> r;
+        r.zero();
+        if (in) r.template load<true>(a.residual, m * a.ld_r + 8 * seg);
+        float v[8];
+        r.get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] += v[i];
+      }
+      if (a.h && in) {
+        Vec8<DT> h;
+        h.set(s[j]);
+        h.template store<false>(a.h, m * a.ld_h + 8 * seg);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq = fmaf(s[j][i], s[j][i], sq);
+    }
+    const float mean = row_sum<TPR>(sq, red, phase) * a.inv_k;
+    const float inv_rms = 1.0f / sqrtf(mean + a.eps);
+    if (a.inv_rms && t == 0) a.inv_rms[m] = inv_rms;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int seg = j * TPR + t;
+      if (seg >= nseg) break;  // whole blocks: K % 32 == 0 keeps 4 adjacent lanes together
+      float w[8], y[8];
+      load_weight(a.weight, a.w_dtype, 8 * seg, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = s[j][i] * inv_rms * w[i];
+      if (a.codes || a.fake) {
+        const uint32_t b = mx8_scale_byte(mx8_amax_bits(y));
+        const u32x2 c = mx8_encode8(y, b);
+        if (a.codes) {
+          *reinterpret_cast<u32x2 *>(a.codes + m * a.K + 8 * seg) = c;
+          if ((seg & 3) == 0) a.scales[m * (a.K / kMx8Blk) + (seg >> 2)] = (uint8_t)b;
+        }
+        if (a.fake) mx8_decode8(c, b, y);
+      }
+      if (a.y) {
+        if (a.y_dtype == 0) {
+          Vec8<0> o;
+          o.set(y);
+          o.store<false>(a.y, m * a.ld_y + 8 * seg);
+        } else {
+          Vec8<1> o;
+          o.set(y);
+          o.store<false>(a.y, m * a.ld_y + 8 * seg);
+        }
+      }
+    }
+  }
+}
+
+// Backward: the rows as above; every thread adds its columns' dy n over the rows it sees, and the
+// workgroup writes one partial row of dweight, [gridDim.x][K] fp32, which k_sum_rows adds in order.
+template <int DT, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_backward(NormGradArgs a) {
+  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+  __shared__ float red[TPR > 64 ? 2 * TPR / 64 : 1];
+  __shared__ float fold[kRows > 1 ? (kRows - 1) * TPR * 8 : 1];
+  const int t = threadIdx.x % TPR;
+  const int nseg = (int)(a.K / 8);
+  float dw[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
+  int phase = 0;
+  for (int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; m < a.M; m += (int64_t)gridDim.x * kRows, ++phase) {
+    const float inv_rms = a.inv_rms[m];
+    float n[NV][8], g[NV][8];
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int seg = j * TPR + t;
+      const bool in = seg < nseg;
+      Vec8<DT> vh, vy;
+      vh.zero();
+      vy.zero();
+      float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (in) {
+        vh.template load<true>(a.h, m * a.ld_h + 8 * seg);
+        vy.template load<true>(a.dy, m * a.ld_dy + 8 * seg);
+        load_weight(a.weight, a.w_dtype, 8 * seg, w);
+      }
+      vh.get(n[j]);
+      vy.get(g[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[j][i] *= inv_rms;
+        dw[j][i] = fmaf(g[j][i], n[j][i], dw[j][i]);
+        g[j][i] *= w[i];
+        dot = fmaf(g[j][i], n[j][i], dot);
+      }
+    }
+    const float c = row_sum<TPR>(dot, red, phase) * a.inv_k;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int seg = j * TPR + t;
+      if (seg >= nseg) break;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = inv_rms * fmaf(-n[j][i], c, g[j][i]);
+      if (a.dh) {
+        Vec8<DT> d;
+        d.template load<true>(a.dh, m * a.ld_dh + 8 * seg);
+        float v[8];
+        d.get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += v[i];
+      }
+      Vec8<DT> q;
+      q.set(o);
+      q.template store<false>(a.dx, m * a.ld_dx + 8 * seg);
+    }
+  }
+  if (!a.partial) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int seg = j * TPR + t;
+    if constexpr (kRows > 1) {  // the workgroup's waves, in order
+      const int r = threadIdx.x / TPR;
+      __syncthreads();
+      if (r > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fold[(r - 1) * TPR * 8 + i * TPR + t] = dw[j][i];
+      }
+      __syncthreads();
+      if (r > 0) continue;
+#pragma unroll
+      for (int q = 0; q < kRows - 1; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[j][i] += fold[q * TPR * 8 + i * TPR + t];
+    }
+    if (seg < nseg) {
+      Vec8<0> o;
+      o.set(dw[j]);
+      o.store<false>(a.partial, (int64_t)blockIdx.x * a.K + 8 * seg);
+    }
+  }
+}
+
+// out[k] = sum over r of partial[r][k]: 8 lanes x 4 columns by 32 row groups per workgroup.
+__global__ __launch_bounds__(256) void k_sum_rows(const float *__restrict__ partial, int rows, int64_t K,
+                                                  float *__restrict__ out) {
+  __shared__ f32x4 part[32][8];
+  const int q = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const int64_t k = (int64_t)blockIdx.x * 32 + 4 * q;
+  f32x4 v = {0, 0, 0, 0};
+  for (int r = r0; r < rows; r += 32) v += *reinterpret_cast<const f32x4 *>(partial + (int64_t)r * K + k);
+  part[r0][q] = v;
+  __syncthreads();
+  if (r0 == 0) {
+    for (int i = 1; i < 32; ++i) v += part[i][q];
+    *reinterpret_cast<f32x4 *>(out + k) = v;
+  }
+}
+
+// ---- launchers --------------------------------------------------------------------------------------
+
+namespace {
+
+int norm_grid(int64_t M, int rows, int cap) {
+  const int64_t g = (M + rows - 1) / rows;
+  return (int)(g < cap ? g : cap);
+}
+
+template <int DT, int TPR>
+hipError_t norm_tpr(const NormArgs &a, hipStream_t s) {
+  constexpr int B = TPR < 256 ? 256 : TPR;
+  const int nv = (int)((a.K / 8 + TPR - 1) / TPR);
+  const int grid = norm_grid(a.M, B / TPR, 1 << 20);
+  switch (nv) {
+    case 1: k_rmsnorm<DT, TPR, 1><<<grid, B, 0, s>>>(a); break;
+    case 2: k_rmsnorm<DT, TPR, 2><<<grid, B, 0, s>>>(a); break;
+    case 3: k_rmsnorm<DT, TPR, 3><<<grid, B, 0, s>>>(a); break;
+    default: k_rmsnorm<DT, TPR, 4><<<grid, B, 0, s>>>(a); break;
+  }
+  return hipGetLastError();
+}
+
+template <int DT, int TPR>
+hipError_t norm_grad_tpr(const NormGradArgs &a, int grid, hipStream_t s) {
+  constexpr int B = TPR < 256 ? 256 : TPR;
+  const int nv = (int)((a.K / 8 + TPR - 1) / TPR);
+  switch (nv) {
+    case 1: k_rmsnorm_backward<DT, TPR, 1><<<grid, B, 0, s>>>(a); break;
+    case 2: k_rmsnorm_backward<DT, TPR, 2><<<grid, B, 0, s>>>(a); break;
+    case 3: k_rmsnorm_backward<DT, TPR, 3><<<grid, B, 0, s>>>(a); break;
+    default: k_rmsnorm_backward<DT, TPR, 4><<<grid, B, 0, s>>>(a); break;
+  }
+  return hipGetLastError();
+}
+
+int threads_per_row(int64_t K) { return K <= 2048 ? 64 : K <= 8192 ? 256 : 1024; }
+
+}  // namespace
+
+int norm_grad_rows(int64_t M, int64_t K) {
+  const int rows = threads_per_row(K) == 64 ? 4 : 1;
+  return norm_grid(M, rows, 512);
+}
+
+hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s) {
+  const int tpr = threads_per_row(a.K);
+  if (a.dtype == 0)
+    return tpr == 64 ? norm_tpr<0, 64>(a, s) : tpr == 256 ? norm_tpr<0, 256>(a, s) : norm_tpr<0, 1024>(a, s);
+  return tpr == 64 ? norm_tpr<1, 64>(a, s) : tpr == 256 ? norm_tpr<1, 256>(a, s) : norm_tpr<1, 1024>(a, s);
+}
+
+hipError_t launch_rmsnorm_backward(const NormGradArgs &a, float *dweight, hipStream_t s) {
+  const int tpr = threads_per_row(a.K), grid = norm_grad_rows(a.M, a.K);
+  if (grid > 0) {
+    hipError_t e;
+    if (a.dtype == 0)
+      e = tpr == 64 ? norm_grad_tpr<0, 64>(a, grid, s) : tpr == 256 ? norm_grad_tpr<0, 256>(a, grid, s)
+                                                                    : norm_grad_tpr<0, 1024>(a, grid, s);
+    else
+      e = tpr == 64 ? norm_grad_tpr<1, 64>(a, grid, s) : tpr == 256 ? norm_grad_tpr<1, 256>(a, grid, s)
+                                                                    : norm_grad_tpr<1, 1024>(a, grid, s);
+    if (e != hipSuccess) return e;
+  }
+  if (!dweight) return hipSuccess;
+  k_sum_rows<<<(unsigned)(a.K / 32), 256, 0, s>>>(a.partial, grid, a.K, dweight);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4
