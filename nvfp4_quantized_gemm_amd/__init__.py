@@ -455,46 +455,52 @@ def nvfp4_mx_gemm(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sc
 ROPE_PAIRS, ROPE_HALVES = 0, 1
 
 
-def _same_device(ref: torch.Tensor, **tensors):
-    """Every given tensor lies on ref's device, which is the current one (the library launches there)."""
-    if not ref.is_cuda:
+def _launch_device(ref: torch.Tensor):
+    """ref's device, which must be the current one (the library launches there)."""
+    dev = ref.device
+    if dev.type != "cuda":
         raise ValueError("the operands must be device tensors")
-    if ref.device.index != torch.cuda.current_device():
-        raise ValueError(f"the operands are on {ref.device}, which is not the current device")
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+    if dev.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the operands are on {dev}, which is not the current device")
+    return dev
 
 
-def _on_stream(stream, *allocated):
+def _on_stream(dev, stream, *allocated) -> int:
     """Raw handle of the stream to launch on; what this call allocated (on the current stream) is kept
     from reuse until that stream is done with it."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream() without making an object
     for t in allocated:
         if t is not None:
             t.record_stream(stream)
     return stream.cuda_stream
 
 
-def _addr(t):
-    return 0 if t is None else t.data_ptr()
+def _dense(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
+    """Address of a dense tensor of the given shape (a tuple), type and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _dense(t: torch.Tensor, name: str, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    return t
-
-
-def _matrix(t: torch.Tensor, name: str, shape, dtype):
-    """Row pitch (elements) of a 2-D tensor of the given shape and type with unit stride along K."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _pitch(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
+    """Row pitch (elements) of a matrix of the given shape, type and device with unit stride along K."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return shape[1]
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit stride along K")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    return ld if shape[0] > 1 else shape[1]
+
+
+def _weight(weight, K: int, dev):
+    """(address, dtype code) of an optional weight vector."""
+    if weight is None:
+        return 0, 0
+    return _dense(weight, "weight", (K,), weight.dtype, dev), _dtype_code(weight.dtype)
 
 
 def nvfp4_mx8_quantize(x: torch.Tensor, *, codes=None, scales=None, stream=None):
@@ -503,15 +509,18 @@ def nvfp4_mx8_quantize(x: torch.Tensor, *, codes=None, scales=None, stream=None)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     M, K = x.shape
-    ld = _matrix(x, "x", (M, K), x.dtype)
-    _same_device(x, codes=codes, scales=scales)
-    codes = torch.empty((M, K), dtype=torch.uint8, device=x.device) if codes is None else \
-        _dense(codes, "codes", (M, K), torch.uint8)
-    scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device) if scales is None else \
-        _dense(scales, "scales", (M, K // 32), torch.uint8)
-    st = lib().nvfp4_mx8_quantize(x.data_ptr(), _dtype_code(x.dtype), M, K, ld, codes.data_ptr(), scales.data_ptr(),
-                                  _on_stream(stream, codes, scales))
-    _check(st, "nvfp4_mx8_quantize")
+    dev = _launch_device(x)
+    ld = _pitch(x, "x", x.shape, x.dtype, dev)
+    if codes is None:
+        codes = torch.empty(M, K, dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(M, K // 32, dtype=torch.uint8, device=dev)
+    st = lib().nvfp4_mx8_quantize(x.data_ptr(), _dtype_code(x.dtype), M, K, ld,
+                                  _dense(codes, "codes", (M, K), torch.uint8, dev),
+                                  _dense(scales, "scales", (M, K // 32), torch.uint8, dev),
+                                  _on_stream(dev, stream, codes, scales))
+    if st:
+        raise NVFP4Error(st, "nvfp4_mx8_quantize")
     return codes, scales
 
 
@@ -535,33 +544,37 @@ def nvfp4_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight:
     without one it is written only into a given h.  save_inv_rms: keep what the backward pass needs."""
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
-    M, K = x.shape
-    dev = x.device
-    ld_x = _matrix(x, "x", (M, K), x.dtype)
-    ld_r = 0 if residual is None else _matrix(residual, "residual", (M, K), x.dtype)
-    _same_device(x, residual=residual, weight=weight, h=h)
-    if weight is not None:
-        _dense(weight, "weight", (K,), weight.dtype)
-    if fake_quantize and y_dtype is None:
-        raise ValueError("fake_quantize needs y_dtype")
-    new_h = None
-    if h is None and residual is not None:
-        h = new_h = torch.empty((M, K), dtype=x.dtype, device=dev)
-    ld_h = 0 if h is None else _matrix(h, "h", (M, K), x.dtype)
-    codes = scales = y = inv_rms = None
+    shape, dtype = x.shape, x.dtype
+    M, K = shape
+    dev = _launch_device(x)
+    ld_x = _pitch(x, "x", shape, dtype, dev)
+    p_r = ld_r = p_h = ld_h = p_c = p_s = p_y = y_code = p_i = 0
+    new_h = codes = scales = y = inv_rms = None
+    if residual is not None:
+        ld_r, p_r = _pitch(residual, "residual", shape, dtype, dev), residual.data_ptr()
+        if h is None:
+            h = new_h = torch.empty(M, K, dtype=dtype, device=dev)
+            ld_h, p_h = K, h.data_ptr()
+    if h is not None and new_h is None:
+        ld_h, p_h = _pitch(h, "h", shape, dtype, dev), h.data_ptr()
+    p_w, w_code = _weight(weight, K, dev)
     if mx8:
-        codes = torch.empty((M, K), dtype=torch.uint8, device=dev)
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
+        codes = torch.empty(M, K, dtype=torch.uint8, device=dev)
+        scales = torch.empty(M, K // 32, dtype=torch.uint8, device=dev)
+        p_c, p_s = codes.data_ptr(), scales.data_ptr()
     if y_dtype is not None:
-        y = torch.empty((M, K), dtype=y_dtype, device=dev)
+        y = torch.empty(M, K, dtype=y_dtype, device=dev)
+        p_y, y_code = y.data_ptr(), _dtype_code(y_dtype)
+    elif fake_quantize:
+        raise ValueError("fake_quantize needs y_dtype")
     if save_inv_rms:
         inv_rms = torch.empty(M, dtype=torch.float32, device=dev)
-    st = lib().nvfp4_rmsnorm(x.data_ptr(), ld_x, _addr(residual), ld_r, _dtype_code(x.dtype), M, K, _addr(weight),
-                             0 if weight is None else _dtype_code(weight.dtype), eps, _addr(h), ld_h, _addr(codes),
-                             _addr(scales), _addr(y), 0 if y is None else _dtype_code(y_dtype), K,
-                             1 if fake_quantize else 0, _addr(inv_rms),
-                             _on_stream(stream, new_h, codes, scales, y, inv_rms))
-    _check(st, "nvfp4_rmsnorm")
+        p_i = inv_rms.data_ptr()
+    st = lib().nvfp4_rmsnorm(x.data_ptr(), ld_x, p_r, ld_r, _dtype_code(dtype), M, K, p_w, w_code, eps, p_h, ld_h, p_c,
+                             p_s, p_y, y_code, K, 1 if fake_quantize else 0, p_i,
+                             _on_stream(dev, stream, new_h, codes, scales, y, inv_rms))
+    if st:
+        raise NVFP4Error(st, "nvfp4_rmsnorm")
     return RMSNormOutput(h, codes, scales, y, inv_rms)
 
 
@@ -577,29 +590,30 @@ def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, inv_rms: torch.Ten
     of x and of residual; dw fp32 [K] is weight's (None with dweight=False)."""
     if h.dim() != 2:
         raise ValueError("h must be 2-D")
-    M, K = h.shape
-    dev = h.device
-    ld_h = _matrix(h, "h", (M, K), h.dtype)
-    ld_dy = _matrix(dy, "dy", (M, K), h.dtype)
-    ld_dh = 0 if dh is None else _matrix(dh, "dh", (M, K), h.dtype)
-    _dense(inv_rms, "inv_rms", (M,), torch.float32)
-    _same_device(h, dy=dy, dh=dh, inv_rms=inv_rms, weight=weight, dx=dx, workspace=workspace)
-    if weight is not None:
-        _dense(weight, "weight", (K,), weight.dtype)
+    shape, dtype = h.shape, h.dtype
+    M, K = shape
+    dev = _launch_device(h)
+    ld_h, ld_dy = _pitch(h, "h", shape, dtype, dev), _pitch(dy, "dy", shape, dtype, dev)
+    ld_dh = 0 if dh is None else _pitch(dh, "dh", shape, dtype, dev)
+    p_i = _dense(inv_rms, "inv_rms", (M,), torch.float32, dev)
+    p_w, w_code = _weight(weight, K, dev)
+    new_dx = new_ws = dw = None
     if dx is None:
-        dx = torch.empty((M, K), dtype=h.dtype, device=dev)
-    ld_dx = _matrix(dx, "dx", (M, K), h.dtype)
-    dw = None
+        dx = new_dx = torch.empty(M, K, dtype=dtype, device=dev)
+    ld_dx = _pitch(dx, "dx", shape, dtype, dev)
+    p_dw = p_ws = ws_bytes = 0
     if dweight:
         dw = torch.empty(K, dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = torch.empty(nvfp4_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().nvfp4_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, _addr(dh), ld_dh, _dtype_code(h.dtype),
-                                      M, K, _addr(weight), 0 if weight is None else _dtype_code(weight.dtype),
-                                      inv_rms.data_ptr(), dx.data_ptr(), ld_dx, _addr(dw), _addr(workspace), ws_bytes,
-                                      _on_stream(stream, dx, dw, workspace))
-    _check(st, "nvfp4_rmsnorm_backward")
+            workspace = new_ws = torch.empty(nvfp4_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+        p_dw, p_ws, ws_bytes = dw.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = lib().nvfp4_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, 0 if dh is None else dh.data_ptr(), ld_dh,
+                                      _dtype_code(dtype), M, K, p_w, w_code, p_i, dx.data_ptr(), ld_dx, p_dw, p_ws,
+                                      ws_bytes, _on_stream(dev, stream, new_dx, dw, new_ws))
+    if st:
+        raise NVFP4Error(st, "nvfp4_rmsnorm_backward")
     return dx, dw
 
 
@@ -646,20 +660,22 @@ def nvfp4_mx_gemm_w4a8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
                        out_dtype: torch.dtype = torch.bfloat16, *, out=None, stream=None) -> torch.Tensor:
     """Y = A B^T with A [M, K] MXFP8 (codes u8 [M, K], scales u8 [M, K/32]) and B [N, K] MXFP4 (packed u8
     [N, K/2], scales u8 [N, K/32]); all dense.  out: a tensor [M, N] (fp32 or bf16, unit stride along N)."""
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b must be 2-D")
     M, K = a.shape
     N = b.shape[0]
-    _dense(a, "a", (M, K), torch.uint8)
-    _dense(a_scales, "a_scales", (M, K // 32), torch.uint8)
-    _dense(b, "b", (N, K // 2), torch.uint8)
-    _dense(b_scales, "b_scales", (N, K // 32), torch.uint8)
-    _same_device(a, a_scales=a_scales, b=b, b_scales=b_scales, out=out)
+    dev = _launch_device(a)
+    u8 = torch.uint8
+    p_a, p_b = _dense(a, "a", (M, K), u8, dev), _dense(b, "b", (N, K // 2), u8, dev)
+    p_as, p_bs = _dense(a_scales, "a_scales", (M, K // 32), u8, dev), _dense(b_scales, "b_scales", (N, K // 32), u8, dev)
     new = None
     if out is None:
-        out = new = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    ldc = _matrix(out, "out", (M, N), out.dtype)
-    st = lib().nvfp4_mx_gemm_w4a8(a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, N, K,
-                                  out.data_ptr(), _dtype_code(out.dtype), ldc, _on_stream(stream, new))
-    _check(st, "nvfp4_mx_gemm_w4a8")
+        out = new = torch.empty(M, N, dtype=out_dtype, device=dev)
+    ldc = _pitch(out, "out", (M, N), out.dtype, dev)
+    st = lib().nvfp4_mx_gemm_w4a8(p_a, p_as, p_b, p_bs, M, N, K, out.data_ptr(), _dtype_code(out.dtype), ldc,
+                                  _on_stream(dev, stream, new))
+    if st:
+        raise NVFP4Error(st, "nvfp4_mx_gemm_w4a8")
     return out
 
 
@@ -678,22 +694,24 @@ def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_fre
     if x.dim() != 3:
         raise ValueError("x must be [T, H, D]")
     T, H, D = x.shape
-    dims = (ctypes.c_int32 * len(axis_dims))(*axis_dims)
-    _dense(positions, "positions", (T, len(axis_dims)), torch.float32)
-    _dense(inv_freq, "inv_freq", (sum(axis_dims) // 2,), torch.float32)
-    _same_device(x, positions=positions, inv_freq=inv_freq, out=out)
+    dev = _launch_device(x)
+    n = len(axis_dims)
+    p_pos = _dense(positions, "positions", (T, n), torch.float32, dev)
+    p_f = _dense(inv_freq, "inv_freq", (sum(axis_dims) // 2,), torch.float32, dev)
     new = None
     if out is None:
-        out = new = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have x's shape and type")
-    if x.stride(2) != 1 or out.stride(2) != 1:
+        out = new = torch.empty(T, H, D, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
+        raise ValueError("out must have x's shape, type and device")
+    xt, xh, xd = x.stride()
+    yt, yh, yd = out.stride()
+    if xd != 1 or yd != 1:
         raise ValueError("x and out must have unit stride along D")
-    st = lib().nvfp4_rope_axes(x.data_ptr(), _dtype_code(x.dtype), T, H, D, x.stride(0), x.stride(1),
-                               positions.data_ptr(), len(axis_dims), dims, inv_freq.data_ptr(), layout,
-                               1 if inverse else 0, out.data_ptr(), out.stride(0), out.stride(1),
-                               _on_stream(stream, new))
-    _check(st, "nvfp4_rope_axes")
+    st = lib().nvfp4_rope_axes(x.data_ptr(), _dtype_code(x.dtype), T, H, D, xt, xh, p_pos, n,
+                               (ctypes.c_int32 * n)(*axis_dims), p_f, layout, 1 if inverse else 0, out.data_ptr(), yt, yh,
+                               _on_stream(dev, stream, new))
+    if st:
+        raise NVFP4Error(st, "nvfp4_rope_axes")
     return out
 
 
