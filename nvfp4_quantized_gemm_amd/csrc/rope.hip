@@ -10,6 +10,8 @@
 // cos and sin are taken once per token and pair, into LDS, for all heads.  The angle is brought to
 // turns with 1/(2 pi) held in two floats, so the reduction is exact to 2^-48 of the angle and
 // large positions lose nothing beyond the angle's own fp32 rounding.
+#include <type_traits>
+
 #include "launch.hpp"
 #include "mx8.hpp"
 
@@ -30,120 +32,232 @@ __device__ __forceinline__ f32x2 turn(float angle) {
   return cs;
 }
 
+// The block's table of cosines and sines, cs[token][pair], in two parts: each thread's first entry's
+// operands are loaded before the tensor's (loads come back in order), the table is filled behind them.
+struct TableEntry {
+  float position, freq;
+};
+__device__ __forceinline__ TableEntry load_entry(const RopeArgs &a, int64_t t0, int i) {
+  const int t = (int)fastdiv((uint32_t)i, a.div_p), p = i - t * a.pairs;
+  int ax = 0;
+  for (int k = 0; k < kRopeMaxAxes - 1; ++k) ax += k < a.n_axes - 1 && p >= a.pair_end[k];
+  return {a.positions[(t0 + t) * a.n_axes + ax], a.inv_freq[p]};
+}
+__device__ __forceinline__ void fill_table(const RopeArgs &a, int64_t t0, int entries, TableEntry e, f32x2 *cs) {
+  for (int i = threadIdx.x; i < entries; i += 256) {
+    if (i >= 256) e = load_entry(a, t0, i);
+    f32x2 v = turn(e.position * e.freq);
+    if (a.inverse) v.y = -v.y;
+    cs[i] = v;
+  }
+}
+
+// V consecutive elements, fp32 or bf16 (2 to 32 bytes; 16-byte accesses at most).
+template <int DT, int V>
+struct Elems {
+  static constexpr int kBytes = V * (DT == 0 ? 4 : 2);
+  typedef typename std::conditional<kBytes == 2, uint16_t, typename std::conditional<kBytes == 4, uint32_t, typename std::conditional<
+      kBytes == 8, u32x2, u32x4>::type>::type>::type Word;
+  static constexpr int kWords = kBytes > 16 ? kBytes / 16 : 1;
+  Word w[kWords];
+  __device__ __forceinline__ void load(const void *base, int64_t elem) {
+    const Word *p = reinterpret_cast<const Word *>(static_cast<const uint8_t *>(base) + elem * (DT == 0 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __builtin_nontemporal_load(p + i);
+  }
+  template <bool NT>
+  __device__ __forceinline__ void store(void *base, int64_t elem) const {
+    Word *p = reinterpret_cast<Word *>(static_cast<uint8_t *>(base) + elem * (DT == 0 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (NT) __builtin_nontemporal_store(w[i], p + i);
+      else p[i] = w[i];
+    }
+  }
+  __device__ __forceinline__ uint32_t word(int i) const {  // 32 bits
+    if constexpr (kBytes <= 4) return w[0];
+    else if constexpr (kBytes == 8) return w[0][i];
+    else return w[i / 4][i % 4];
+  }
+  __device__ __forceinline__ void set_word(int i, uint32_t v) {
+    if constexpr (kBytes <= 4) w[0] = (Word)v;
+    else if constexpr (kBytes == 8) w[0][i] = v;
+    else w[i / 4][i % 4] = v;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (DT == 0) return __uint_as_float(word(i));
+    else return (i & 1) ? bf16hi(word(i / 2)) : bf16lo(word(i / 2));
+  }
+  __device__ __forceinline__ void set(const float (&v)[V]) {
+    if constexpr (DT == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) set_word(i, __float_as_uint(v[i]));
+    } else if constexpr (V == 1) {
+      w[0] = __builtin_bit_cast(uint16_t, (__bf16)v[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const bf16x2 h = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
+        set_word(i, __builtin_bit_cast(uint32_t, h));
+      }
+    }
+  }
+};
+
+}  // namespace
+
+// One workgroup turns `tokens` consecutive tokens, 256 x B units at a time.  Layout pairs: a unit is 8
+// elements (4 pairs).
+template <int DT, bool NT>
+__global__ __launch_bounds__(256) void k_rope_pairs(RopeArgs a) {
+  constexpr int B = 4;
+  extern __shared__ f32x2 cs[];
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int nt = (int)min((int64_t)a.tokens, a.T - t0);
+  const int C = a.D / 8, n = nt * a.H * C, entries = nt * a.pairs;
+  TableEntry e = {0.0f, 0.0f};
+  if ((int)threadIdx.x < entries) e = load_entry(a, t0, threadIdx.x);
+  for (int base = 0; base < n; base += 256 * B) {
+    Elems<DT, 8> v[B];
+    int tt[B], cc[B], hh[B];
+#pragma unroll
+    for (int q = 0; q < B; ++q) {
+      const int i = base + 256 * q + threadIdx.x;
+      const int row = (int)fastdiv((uint32_t)i, a.div_c);
+      cc[q] = i - row * C;
+      tt[q] = (int)fastdiv((uint32_t)row, a.div_h);
+      hh[q] = row - tt[q] * a.H;
+      if (i < n) v[q].load(a.x, (t0 + tt[q]) * a.ld_t + hh[q] * a.ld_h + 8 * cc[q]);
+    }
+    if (base == 0) {
+      fill_table(a, t0, entries, e, cs);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < B; ++q) {
+      if (base + 256 * q + (int)threadIdx.x >= n) break;
+      float y[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int p = 4 * cc[q] + k;
+        const float x1 = v[q].get(2 * k), x2 = v[q].get(2 * k + 1);
+        y[2 * k] = x1;  // past the sections: as it is
+        y[2 * k + 1] = x2;
+        if (p < a.pairs) {
+          const f32x2 r = cs[tt[q] * a.pairs + p];
+          y[2 * k] = x1 * r.x - x2 * r.y;
+          y[2 * k + 1] = x2 * r.x + x1 * r.y;
+        }
+      }
+      v[q].set(y);
+      v[q].template store<NT>(a.y, (t0 + tt[q]) * a.ldy_t + hh[q] * a.ldy_h + 8 * cc[q]);
+    }
+  }
+}
+
+// Layout halves: a unit is V consecutive pairs, i.e. V elements and the V half a section on.  V is the
+// largest of 8, 4, 2, 1 that divides every half section (and half of what lies past the sections, which is
+// copied as pairs of its own).
+template <int DT, int V, bool NT>
+__global__ __launch_bounds__(256) void k_rope_halves(RopeArgs a) {
+  constexpr int B = V <= 2 ? 8 : 4;
+  extern __shared__ f32x2 cs[];
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int nt = (int)min((int64_t)a.tokens, a.T - t0);
+  const int C = a.D / (2 * V), n = nt * a.H * C, entries = nt * a.pairs;
+  TableEntry e = {0.0f, 0.0f};
+  if ((int)threadIdx.x < entries) e = load_entry(a, t0, threadIdx.x);
+  for (int base = 0; base < n; base += 256 * B) {
+    Elems<DT, V> v[B][2];
+    int tt[B], pp[B], hh[B], e1[B], e2[B];
+#pragma unroll
+    for (int q = 0; q < B; ++q) {
+      const int i = base + 256 * q + threadIdx.x;
+      const int row = (int)fastdiv((uint32_t)i, a.div_c);
+      const int p = (i - row * C) * V;
+      int p0 = 0, end = a.pair_end[0];  // the section's pairs; past the sections: the rest of the head's
+#pragma unroll
+      for (int k = 0; k < kRopeMaxAxes; ++k) {
+        if (k < a.n_axes && p >= a.pair_end[k]) {
+          p0 = a.pair_end[k];
+          end = k + 1 < a.n_axes ? a.pair_end[k + 1 < kRopeMaxAxes ? k + 1 : k] : a.D / 2;
+        }
+      }
+      pp[q] = p;
+      e1[q] = p + p0;  // the section starts at element 2 p0
+      e2[q] = p + end;
+      tt[q] = (int)fastdiv((uint32_t)row, a.div_h);
+      hh[q] = row - tt[q] * a.H;
+      if (i < n) {
+        const int64_t src = (t0 + tt[q]) * a.ld_t + hh[q] * a.ld_h;
+        v[q][0].load(a.x, src + e1[q]);
+        v[q][1].load(a.x, src + e2[q]);
+      }
+    }
+    if (base == 0) {
+      fill_table(a, t0, entries, e, cs);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < B; ++q) {
+      if (base + 256 * q + (int)threadIdx.x >= n) break;
+      if (pp[q] < a.pairs) {
+        float y1[V], y2[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const f32x2 r = cs[tt[q] * a.pairs + pp[q] + k];
+          const float x1 = v[q][0].get(k), x2 = v[q][1].get(k);
+          y1[k] = x1 * r.x - x2 * r.y;
+          y2[k] = x2 * r.x + x1 * r.y;
+        }
+        v[q][0].set(y1);
+        v[q][1].set(y2);
+      }
+      const int64_t dst = (t0 + tt[q]) * a.ldy_t + hh[q] * a.ldy_h;
+      v[q][0].template store<NT>(a.y, dst + e1[q]);
+      v[q][1].template store<NT>(a.y, dst + e2[q]);
+    }
+  }
+}
+
+namespace {
+
+template <int DT, bool NT>
+hipError_t launch_layout(const RopeArgs &a, int V, unsigned grid, size_t lds, hipStream_t s) {
+  if (!a.halves) k_rope_pairs<DT, NT><<<grid, 256, lds, s>>>(a);
+  else if (V == 8) k_rope_halves<DT, 8, NT><<<grid, 256, lds, s>>>(a);
+  else if (V == 4) k_rope_halves<DT, 4, NT><<<grid, 256, lds, s>>>(a);
+  else if (V == 2) k_rope_halves<DT, 2, NT><<<grid, 256, lds, s>>>(a);
+  else k_rope_halves<DT, 1, NT><<<grid, 256, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+// Streaming stores above 128 MB, half the last-level cache, where the result would not be there for its
+// reader anyway (10240 x 64 x 128 bf16, 168 MB: 56.9 us and 60.4); below they cost time (4097 x 32 x 72
+// fp32, 38 MB: 20.1 us and 18.9).
 template <int DT>
-__device__ __forceinline__ float get1(const void *p, int64_t e) {
-  return DT == 0 ? static_cast<const float *>(p)[e] : bf16lo(static_cast<const uint16_t *>(p)[e]);
+hipError_t launch_dtype(const RopeArgs &a, int V, unsigned grid, size_t lds, hipStream_t s) {
+  const bool stream = a.T * a.H * a.D * (DT == 0 ? 4 : 2) > (int64_t(128) << 20);
+  return stream ? launch_layout<DT, true>(a, V, grid, lds, s) : launch_layout<DT, false>(a, V, grid, lds, s);
 }
 
 }  // namespace
 
-// One workgroup turns `tokens` consecutive tokens.  cs[token][pair] in LDS.  Layout pairs: a lane
-// takes 8 elements (4 pairs) at a time.
-template <int DT>
-__global__ __launch_bounds__(256) void k_rope_pairs(RopeArgs a) {
-  extern __shared__ f32x2 cs[];
-  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
-  const int nt = (int)min((int64_t)a.tokens, a.T - t0);
-  for (int i = threadIdx.x; i < nt * a.pairs; i += 256) {
-    const int t = i / a.pairs, p = i - t * a.pairs;
-    int ax = 0;
-    while (p >= a.pair_end[ax]) ++ax;
-    f32x2 v = turn(a.positions[(t0 + t) * a.n_axes + ax] * a.inv_freq[p]);
-    if (a.inverse) v.y = -v.y;
-    cs[i] = v;
-  }
-  __syncthreads();
-  const int C = a.D / 8, n = nt * a.H * C;
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int row = (int)fastdiv((uint32_t)i, a.div_c), c = i - row * C;
-    const int t = (int)fastdiv((uint32_t)row, a.div_h), h = row - t * a.H;
-    Vec8<DT> v;
-    v.template load<true>(a.x, (t0 + t) * a.ld_t + h * a.ld_h + 8 * c);
-    float x[8];
-    v.get(x);
-    float y[8];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int p = 4 * c + q;
-      if (p < a.pairs) {
-        const f32x2 r = cs[t * a.pairs + p];
-        y[2 * q] = x[2 * q] * r.x - x[2 * q + 1] * r.y;
-        y[2 * q + 1] = x[2 * q + 1] * r.x + x[2 * q] * r.y;
-      } else {
-        y[2 * q] = x[2 * q];
-        y[2 * q + 1] = x[2 * q + 1];
-      }
-    }
-    v.set(y);
-    v.template store<false>(a.y, (t0 + t) * a.ldy_t + h * a.ldy_h + 8 * c);
-  }
-}
-
-// Layout halves: a lane takes one pair; the elements past the sections are copied as pairs of their own.
-template <int DT>
-__global__ __launch_bounds__(256) void k_rope_halves(RopeArgs a) {
-  extern __shared__ f32x2 cs[];
-  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
-  const int nt = (int)min((int64_t)a.tokens, a.T - t0);
-  for (int i = threadIdx.x; i < nt * a.pairs; i += 256) {
-    const int t = i / a.pairs, p = i - t * a.pairs;
-    int ax = 0;
-    while (p >= a.pair_end[ax]) ++ax;
-    f32x2 v = turn(a.positions[(t0 + t) * a.n_axes + ax] * a.inv_freq[p]);
-    if (a.inverse) v.y = -v.y;
-    cs[i] = v;
-  }
-  __syncthreads();
-  const int C = a.D / 2, n = nt * a.H * C;
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int row = i / C, p = i - row * C;
-    const int t = (int)fastdiv((uint32_t)row, a.div_h), h = row - t * a.H;
-    const int64_t src = (t0 + t) * a.ld_t + h * a.ld_h, dst = (t0 + t) * a.ldy_t + h * a.ldy_h;
-    int e1, e2;
-    float c = 1.0f, s = 0.0f;
-    if (p < a.pairs) {
-      int ax = 0;
-      while (p >= a.pair_end[ax]) ++ax;
-      const int p0 = ax ? a.pair_end[ax - 1] : 0;
-      e1 = p + p0;  // the section starts at element 2 p0
-      e2 = e1 + a.pair_end[ax] - p0;
-      c = cs[t * a.pairs + p].x;
-      s = cs[t * a.pairs + p].y;
-    } else {
-      e1 = 2 * p;
-      e2 = e1 + 1;
-    }
-    const float x1 = get1<DT>(a.x, src + e1), x2 = get1<DT>(a.x, src + e2);
-    const bool pass = p >= a.pairs;
-    const float y1 = pass ? x1 : x1 * c - x2 * s, y2 = pass ? x2 : x2 * c + x1 * s;
-    if (DT == 0) {
-      static_cast<float *>(a.y)[dst + e1] = y1;
-      static_cast<float *>(a.y)[dst + e2] = y2;
-    } else {
-      static_cast<__bf16 *>(a.y)[dst + e1] = (__bf16)y1;
-      static_cast<__bf16 *>(a.y)[dst + e2] = (__bf16)y2;
-    }
-  }
-}
-
 hipError_t launch_rope(RopeArgs a, hipStream_t s) {
-  // about 1024 vectors of 8 elements per workgroup, at least one token
+  // about 1024 units of 16 bytes per workgroup, at least one token
   const int64_t per = (int64_t)a.H * (a.D / 8);
   int64_t tokens = per >= 1024 ? 1 : 1024 / per;
   if (tokens > 16) tokens = 16;
   a.tokens = (int)tokens;
-  a.div_c = make_fastdiv((uint32_t)(a.D / 8));
+  int bits = 8 | (a.D / 2 - a.pairs);  // with half of what lies past the sections
+  for (int i = 0, p0 = 0; i < a.n_axes; p0 = a.pair_end[i++]) bits |= a.pair_end[i] - p0;
+  const int V = bits & -bits;
+  a.div_c = make_fastdiv((uint32_t)(a.halves ? a.D / (2 * V) : a.D / 8));
   a.div_h = make_fastdiv((uint32_t)a.H);
+  a.div_p = make_fastdiv((uint32_t)(a.pairs > 0 ? a.pairs : 1));
   const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
   const size_t lds = (size_t)tokens * a.pairs * sizeof(f32x2);
-  if (a.halves) {
-    if (a.dtype == 0) k_rope_halves<0><<<grid, 256, lds, s>>>(a);
-    else k_rope_halves<1><<<grid, 256, lds, s>>>(a);
-  } else {
-    if (a.dtype == 0) k_rope_pairs<0><<<grid, 256, lds, s>>>(a);
-    else k_rope_pairs<1><<<grid, 256, lds, s>>>(a);
-  }
-  return hipGetLastError();
+  return a.dtype == 0 ? launch_dtype<0>(a, V, grid, lds, s) : launch_dtype<1>(a, V, grid, lds, s);
 }
 
 }  // namespace nvfp4
