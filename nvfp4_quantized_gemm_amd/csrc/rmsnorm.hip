@@ -61,42 +61,61 @@ __device__ __forceinline__ void load_weight(const void *w, int w_dtype, int64_t 
 }  // namespace
 
 // TPR threads (64, 256 or 1024) hold a row in registers, NV vectors of 8 elements each; workgroups
-// of 256 threads take 4 rows at TPR = 64.
-template <int DT, int TPR, int NV>
+// of 256 threads take 4 rows at TPR = 64.  A workgroup walks over rows with the weight in registers
+// and the next row's loads in flight while it works on one.
+template <int DT, int TPR, int NV, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
   constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+  constexpr bool kAhead = TPR < 1024 || NV <= 2;  // 16 waves leave 128 registers: none to look ahead
   __shared__ float red[TPR > 64 ? 2 * TPR / 64 : 1];
   const int t = threadIdx.x % TPR;
   const int nseg = (int)(a.K / 8);
-  int phase = 0;
-  for (int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; m < a.M; m += (int64_t)gridDim.x * kRows, ++phase) {
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  Vec8<DT> x[NV], r[NV];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int seg = j * TPR + t;
+      x[j].zero();
+      r[j].zero();
+      if (seg < nseg) {
+        x[j].template load<true>(a.x, row * a.ld_x + 8 * seg);
+        if (a.residual) r[j].template load<true>(a.residual, row * a.ld_r + 8 * seg);
+      }
+    }
+  };
+  if (kAhead && m < a.M) fetch(m);
+  float w[kAhead ? NV : 1][8];
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int seg = j * TPR + t;
+      load_weight(a.weight, a.w_dtype, 8 * (seg < nseg ? seg : 0), w[j]);
+    }
+  }
+  for (int phase = 0; m < a.M; m += step, ++phase) {
+    if constexpr (!kAhead) fetch(m);
     float s[NV][8];
     float sq = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int seg = j * TPR + t;
-      const bool in = seg < nseg;
-      Vec8<DT> x;
-      x.zero();
-      if (in) x.template load<true>(a.x, m * a.ld_x + 8 * seg);
-      x.get(s[j]);
-      if (a.residual) {
-        Vec8<DT> r;
-        r.zero();
-        if (in) r.template load<true>(a.residual, m * a.ld_r + 8 * seg);
-        float v[8];
-        r.get(v);
+      float v[8];
+      x[j].get(s[j]);
+      r[j].get(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[j][i] += v[i];
+      for (int i = 0; i < 8; ++i) {
+        s[j][i] += v[i];
+        sq = fmaf(s[j][i], s[j][i], sq);
       }
-      if (a.h && in) {
+      if (a.h && seg < nseg) {
         Vec8<DT> h;
         h.set(s[j]);
-        h.template store<false>(a.h, m * a.ld_h + 8 * seg);
+        h.template store<NT>(a.h, m * a.ld_h + 8 * seg);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(s[j][i], s[j][i], sq);
     }
+    if (kAhead && m + step < a.M) fetch(m + step);
     const float mean = row_sum<TPR>(sq, red, phase) * a.inv_k;
     const float inv_rms = 1.0f / sqrtf(mean + a.eps);
     if (a.inv_rms && t == 0) a.inv_rms[m] = inv_rms;
@@ -104,15 +123,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
     for (int j = 0; j < NV; ++j) {
       const int seg = j * TPR + t;
       if (seg >= nseg) break;  // whole blocks: K % 32 == 0 keeps 4 adjacent lanes together
-      float w[8], y[8];
-      load_weight(a.weight, a.w_dtype, 8 * seg, w);
+      float y[8];
+      float(&wj)[8] = w[kAhead ? j : 0];
+      if constexpr (!kAhead) load_weight(a.weight, a.w_dtype, 8 * seg, wj);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = s[j][i] * inv_rms * w[i];
+      for (int i = 0; i < 8; ++i) y[i] = s[j][i] * inv_rms * wj[i];
       if (a.codes || a.fake) {
         const uint32_t b = mx8_scale_byte(mx8_amax_bits(y));
         const u32x2 c = mx8_encode8(y, b);
         if (a.codes) {
-          *reinterpret_cast<u32x2 *>(a.codes + m * a.K + 8 * seg) = c;
+          u32x2 *const to = reinterpret_cast<u32x2 *>(a.codes + m * a.K + 8 * seg);
+          if constexpr (NT) __builtin_nontemporal_store(c, to);
+          else *to = c;
           if ((seg & 3) == 0) a.scales[m * (a.K / kMx8Blk) + (seg >> 2)] = (uint8_t)b;
         }
         if (a.fake) mx8_decode8(c, b, y);
@@ -121,11 +143,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
         if (a.y_dtype == 0) {
           Vec8<0> o;
           o.set(y);
-          o.store<false>(a.y, m * a.ld_y + 8 * seg);
+          o.store<NT>(a.y, m * a.ld_y + 8 * seg);
         } else {
           Vec8<1> o;
           o.set(y);
-          o.store<false>(a.y, m * a.ld_y + 8 * seg);
+          o.store<NT>(a.y, m * a.ld_y + 8 * seg);
         }
       }
     }
@@ -134,65 +156,77 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
 
 // Backward: the rows as above; every thread adds its columns' dy n over the rows it sees, and the
 // workgroup writes one partial row of dweight, [gridDim.x][K] fp32, which k_sum_rows adds in order.
-template <int DT, int TPR, int NV>
+template <int DT, int TPR, int NV, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_backward(NormGradArgs a) {
   constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+  constexpr bool kAhead = TPR < 1024;
   __shared__ float red[TPR > 64 ? 2 * TPR / 64 : 1];
   __shared__ float fold[kRows > 1 ? (kRows - 1) * TPR * 8 : 1];
   const int t = threadIdx.x % TPR;
   const int nseg = (int)(a.K / 8);
-  float dw[NV][8];
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  Vec8<DT> vh[NV], vy[NV], vd[NV];
+  float next_rms = 0.0f;
+  auto fetch = [&](int64_t row) {
+    next_rms = a.inv_rms[row];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const int seg = j * TPR + t;
+      vh[j].zero();
+      vy[j].zero();
+      vd[j].zero();
+      if (seg < nseg) {
+        vh[j].template load<true>(a.h, row * a.ld_h + 8 * seg);
+        vy[j].template load<true>(a.dy, row * a.ld_dy + 8 * seg);
+        if (a.dh) vd[j].template load<true>(a.dh, row * a.ld_dh + 8 * seg);
+      }
+    }
+  };
+  if (kAhead && m < a.M) fetch(m);
+  float w[kAhead ? NV : 1][8], dw[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int seg = j * TPR + t;
+    if constexpr (kAhead) load_weight(a.weight, a.w_dtype, 8 * (seg < nseg ? seg : 0), w[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-  int phase = 0;
-  for (int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; m < a.M; m += (int64_t)gridDim.x * kRows, ++phase) {
-    const float inv_rms = a.inv_rms[m];
+  }
+  for (int phase = 0; m < a.M; m += step, ++phase) {
+    if constexpr (!kAhead) fetch(m);
+    const float inv_rms = next_rms;
     float n[NV][8], g[NV][8];
+    Vec8<DT> d[NV];
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int seg = j * TPR + t;
-      const bool in = seg < nseg;
-      Vec8<DT> vh, vy;
-      vh.zero();
-      vy.zero();
-      float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (in) {
-        vh.template load<true>(a.h, m * a.ld_h + 8 * seg);
-        vy.template load<true>(a.dy, m * a.ld_dy + 8 * seg);
-        load_weight(a.weight, a.w_dtype, 8 * seg, w);
-      }
-      vh.get(n[j]);
-      vy.get(g[j]);
+      float(&wj)[8] = w[kAhead ? j : 0];
+      if constexpr (!kAhead) load_weight(a.weight, a.w_dtype, 8 * (seg < nseg ? seg : 0), wj);
+      vh[j].get(n[j]);
+      vy[j].get(g[j]);
+      d[j] = vd[j];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         n[j][i] *= inv_rms;
         dw[j][i] = fmaf(g[j][i], n[j][i], dw[j][i]);
-        g[j][i] *= w[i];
+        g[j][i] *= wj[i];
         dot = fmaf(g[j][i], n[j][i], dot);
       }
     }
+    if (kAhead && m + step < a.M) fetch(m + step);
     const float c = row_sum<TPR>(dot, red, phase) * a.inv_k;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int seg = j * TPR + t;
       if (seg >= nseg) break;
       float o[8];
+      d[j].get(o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = inv_rms * fmaf(-n[j][i], c, g[j][i]);
-      if (a.dh) {
-        Vec8<DT> d;
-        d.template load<true>(a.dh, m * a.ld_dh + 8 * seg);
-        float v[8];
-        d.get(v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += v[i];
-      }
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(inv_rms, fmaf(-n[j][i], c, g[j][i]), o[i]);
       Vec8<DT> q;
       q.set(o);
-      q.template store<false>(a.dx, m * a.ld_dx + 8 * seg);
+      q.template store<NT>(a.dx, m * a.ld_dx + 8 * seg);
     }
   }
   if (!a.partial) return;
@@ -221,18 +255,28 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_backward(Norm
   }
 }
 
-// out[k] = sum over r of partial[r][k]: 8 lanes x 4 columns by 32 row groups per workgroup.
-__global__ __launch_bounds__(256) void k_sum_rows(const float *__restrict__ partial, int rows, int64_t K,
-                                                  float *__restrict__ out) {
-  __shared__ f32x4 part[32][8];
+// out[k] = sum over r of partial[r][k]: 8 lanes x 4 columns by 128 row groups per workgroup, whose
+// sums are added in order.
+__global__ __launch_bounds__(1024) void k_sum_rows(const float *__restrict__ partial, int rows, int64_t K,
+                                                   float *__restrict__ out) {
+  __shared__ f32x4 part[128][8];
   const int q = threadIdx.x & 7, r0 = threadIdx.x >> 3;
   const int64_t k = (int64_t)blockIdx.x * 32 + 4 * q;
   f32x4 v = {0, 0, 0, 0};
-  for (int r = r0; r < rows; r += 32) v += *reinterpret_cast<const f32x4 *>(partial + (int64_t)r * K + k);
+#pragma unroll 4
+  for (int r = r0; r < rows; r += 128) v += *reinterpret_cast<const f32x4 *>(partial + (int64_t)r * K + k);
   part[r0][q] = v;
   __syncthreads();
+  if (r0 < 8) {
+    v = part[r0][q];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += part[r0 + 8 * i][q];
+    part[r0][q] = v;
+  }
+  __syncthreads();
   if (r0 == 0) {
-    for (int i = 1; i < 32; ++i) v += part[i][q];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += part[i][q];
     *reinterpret_cast<f32x4 *>(out + k) = v;
   }
 }
@@ -246,51 +290,71 @@ int norm_grid(int64_t M, int rows, int cap) {
   return (int)(g < cap ? g : cap);
 }
 
+// Streaming stores from 8 MB of results on (4096 x 1152 bf16: 7.8 us and 10.2; 16384 x 8192: 163 and 180);
+// below they cost time (512 x 4096: 5.5 us and 5.2).
+bool streams(int64_t bytes) { return bytes > (int64_t(8) << 20); }
+
+template <int DT, int TPR, int NV>
+hipError_t norm_nv(const NormArgs &a, hipStream_t s) {
+  constexpr int B = TPR < 256 ? 256 : TPR;
+  const int grid = norm_grid(a.M, B / TPR, 2048);
+  const int64_t per = (a.h ? (DT == 0 ? 4 : 2) : 0) + (a.codes ? 1 : 0) + (a.y ? (a.y_dtype == 0 ? 4 : 2) : 0);
+  if (streams(per * a.M * a.K)) k_rmsnorm<DT, TPR, NV, true><<<grid, B, 0, s>>>(a);
+  else k_rmsnorm<DT, TPR, NV, false><<<grid, B, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <int DT, int TPR>
 hipError_t norm_tpr(const NormArgs &a, hipStream_t s) {
-  constexpr int B = TPR < 256 ? 256 : TPR;
-  const int nv = (int)((a.K / 8 + TPR - 1) / TPR);
-  const int grid = norm_grid(a.M, B / TPR, 1 << 20);
-  switch (nv) {
-    case 1: k_rmsnorm<DT, TPR, 1><<<grid, B, 0, s>>>(a); break;
-    case 2: k_rmsnorm<DT, TPR, 2><<<grid, B, 0, s>>>(a); break;
-    case 3: k_rmsnorm<DT, TPR, 3><<<grid, B, 0, s>>>(a); break;
-    default: k_rmsnorm<DT, TPR, 4><<<grid, B, 0, s>>>(a); break;
+  switch ((a.K / 8 + TPR - 1) / TPR) {
+    case 1: return norm_nv<DT, TPR, 1>(a, s);
+    case 2: return norm_nv<DT, TPR, 2>(a, s);
+    case 3: return norm_nv<DT, TPR, 3>(a, s);
+    default: return norm_nv<DT, TPR, 4>(a, s);
   }
+}
+
+template <int DT, int TPR, int NV>
+hipError_t norm_grad_nv(const NormGradArgs &a, int grid, hipStream_t s) {
+  constexpr int B = TPR < 256 ? 256 : TPR;
+  if (streams(a.M * a.K * (DT == 0 ? 4 : 2))) k_rmsnorm_backward<DT, TPR, NV, true><<<grid, B, 0, s>>>(a);
+  else k_rmsnorm_backward<DT, TPR, NV, false><<<grid, B, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <int DT, int TPR>
 hipError_t norm_grad_tpr(const NormGradArgs &a, int grid, hipStream_t s) {
-  constexpr int B = TPR < 256 ? 256 : TPR;
-  const int nv = (int)((a.K / 8 + TPR - 1) / TPR);
-  switch (nv) {
-    case 1: k_rmsnorm_backward<DT, TPR, 1><<<grid, B, 0, s>>>(a); break;
-    case 2: k_rmsnorm_backward<DT, TPR, 2><<<grid, B, 0, s>>>(a); break;
-    case 3: k_rmsnorm_backward<DT, TPR, 3><<<grid, B, 0, s>>>(a); break;
-    default: k_rmsnorm_backward<DT, TPR, 4><<<grid, B, 0, s>>>(a); break;
+  switch ((a.K / 8 + TPR - 1) / TPR) {
+    case 1: return norm_grad_nv<DT, TPR, 1>(a, grid, s);
+    case 2: return norm_grad_nv<DT, TPR, 2>(a, grid, s);
+    case 3: return norm_grad_nv<DT, TPR, 3>(a, grid, s);
+    default: return norm_grad_nv<DT, TPR, 4>(a, grid, s);
   }
-  return hipGetLastError();
 }
 
-int threads_per_row(int64_t K) { return K <= 2048 ? 64 : K <= 8192 ? 256 : 1024; }
+// A wave to a row where the row fits its registers; else a workgroup of 256, or, where K is larger or the
+// rows are too few to fill the chip, of 1024 (one row of 4608: 3.7 us and 3.9).
+int threads_per_row(int64_t M, int64_t K) { return K <= 2048 ? 64 : K <= 8192 && M > 256 ? 256 : 1024; }
 
 }  // namespace
 
 int norm_grad_rows(int64_t M, int64_t K) {
-  const int rows = threads_per_row(K) == 64 ? 4 : 1;
-  return norm_grid(M, rows, 512);
+  // One workgroup per CU, two where each then still has eight turns: fewer leave CUs idle, more write and
+  // add more partial rows (4096 x 1152: 128, 256, 512, 1024 workgroups 15.9, 13.2, 13.7, 17.6 us; 10240 x
+  // 4608: 102, 71.8, 70.2, 74.6; 512 x 4096: 10.9, 10.5, 13.7).
+  const int64_t turns = threads_per_row(M, K) == 64 ? (M + 3) / 4 : M;
+  return (int)(turns < 256 ? turns : turns < 8 * 256 ? 256 : turns < 8 * 512 ? turns / 8 : 512);
 }
 
 hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s) {
-  const int tpr = threads_per_row(a.K);
+  const int tpr = threads_per_row(a.M, a.K);
   if (a.dtype == 0)
     return tpr == 64 ? norm_tpr<0, 64>(a, s) : tpr == 256 ? norm_tpr<0, 256>(a, s) : norm_tpr<0, 1024>(a, s);
   return tpr == 64 ? norm_tpr<1, 64>(a, s) : tpr == 256 ? norm_tpr<1, 256>(a, s) : norm_tpr<1, 1024>(a, s);
 }
 
 hipError_t launch_rmsnorm_backward(const NormGradArgs &a, float *dweight, hipStream_t s) {
-  const int tpr = threads_per_row(a.K), grid = norm_grad_rows(a.M, a.K);
+  const int tpr = threads_per_row(a.M, a.K), grid = norm_grad_rows(a.M, a.K);
   if (grid > 0) {
     hipError_t e;
     if (a.dtype == 0)
@@ -302,7 +366,7 @@ hipError_t launch_rmsnorm_backward(const NormGradArgs &a, float *dweight, hipStr
     if (e != hipSuccess) return e;
   }
   if (!dweight) return hipSuccess;
-  k_sum_rows<<<(unsigned)(a.K / 32), 256, 0, s>>>(a.partial, grid, a.K, dweight);
+  k_sum_rows<<<(unsigned)(a.K / 32), 1024, 0, s>>>(a.partial, grid, a.K, dweight);
   return hipGetLastError();
 }
 
