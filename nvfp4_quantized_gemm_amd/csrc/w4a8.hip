@@ -10,21 +10,33 @@
 
 namespace nvfp4 {
 
-// A lane takes 8 consecutive elements, 4 adjacent lanes a block.
+// A lane takes 8 consecutive elements, 4 adjacent lanes a block, and has two such segments in flight.
+// Bound by memory, 3.03 B per bf16 element: 16384 x 8192 in 61 us (6.6 TB/s; one segment 70, four 63), 4096 x
+// 4608 in 11.6 us (12.6, 11.5), 4096 x 1152 in 4.3 us (4.4, 4.7).
 template <int DT, bool DENSE>
 __global__ __launch_bounds__(256) void k_mx8_quantize(const void *__restrict__ x, int64_t ld, uint64_t nseg,
                                                       FastDiv bpr, uint8_t *__restrict__ codes,
                                                       uint8_t *__restrict__ scales) {
-  for (uint64_t g = blockIdx.x * 256ull + threadIdx.x; g < nseg; g += gridDim.x * 256ull) {
+  constexpr int U = 2;
+  const uint64_t g0 = (uint64_t)blockIdx.x * (256 * U) + threadIdx.x;
+  Vec8<DT> v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint64_t g = g0 + 256 * u;
+    if (g >= nseg) break;
     int64_t off = (int64_t)g * 8;
     if (!DENSE) {
       const uint32_t blk = (uint32_t)(g >> 2), row = fastdiv(blk, bpr);
       off = (int64_t)row * ld + (int64_t)(blk - row * bpr.d) * kMx8Blk + 8 * (int64_t)(g & 3);
     }
-    Vec8<DT> v;
-    v.template load<true>(x, off);
+    v[u].template load<true>(x, off);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint64_t g = g0 + 256 * u;
+    if (g >= nseg) break;  // whole blocks are in or out
     float f[8];
-    v.get(f);
+    v[u].get(f);
     const uint32_t b = mx8_scale_byte(mx8_amax_bits(f));
     *reinterpret_cast<u32x2 *>(codes + 8 * g) = mx8_encode8(f, b);
     if ((g & 3) == 0) scales[g >> 2] = (uint8_t)b;
@@ -651,8 +663,7 @@ hipError_t launch_mx8_quantize(const void *x, int dtype, int64_t M, int64_t K, i
                                uint8_t *scales, hipStream_t s) {
   const FastDiv bpr = make_fastdiv((uint32_t)(K / kMx8Blk));
   const uint64_t nseg = (uint64_t)M * (uint64_t)K / 8;
-  uint64_t g = (nseg + 255) / 256;
-  const unsigned grid = (unsigned)(g > 16384 ? 16384 : g);
+  const unsigned grid = (unsigned)((nseg + 511) / 512);
   const bool dense = ld == K;
   if (dtype == 0) {
     if (dense) k_mx8_quantize<0, true><<<grid, 256, 0, s>>>(x, ld, nseg, bpr, codes, scales);
