@@ -353,8 +353,8 @@ nvfp4_status_t nvfp4_mx_gemm(const uint8_t *a, const uint8_t *a_scales, const ui
  * K share one E8M0 scale byte b (X = 2^(b - 127)), X = 2^(floor(log2 amax) - 8) with b clamped to
  * [0, 246] and b = 0 for an all-zero block; each value is the E4M3FN code nearest to v / X (ties to
  * even, saturating at +-448).  codes are bytes [M][K], scales bytes [M][K/32], both dense.  A block
- * that holds an infinity or a NaN gets b = 255 and zero codes (other blocks are not touched by it).
- * K >= 32, K % 32 == 0.
+ * that holds an infinity or a NaN gets b = 255 and NaN codes (0x7F); other blocks are not touched by
+ * it, and of a product only that row's outputs become NaN.  K >= 32, K % 32 == 0.
  *
  * Pitches (ld_*) are elements from one row to the next; every fp32 or bf16 array is 16-byte
  * aligned with a pitch of whole 16 bytes, except where a call says otherwise.  NVFP4_ERR_SHAPE also

@@ -13,6 +13,7 @@ from enum import IntEnum
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
@@ -465,15 +466,10 @@ def _launch_device(ref: torch.Tensor):
     return dev
 
 
-def _on_stream(dev, stream, *allocated) -> int:
-    """Raw handle of the stream to launch on; what this call allocated (on the current stream) is kept
-    from reuse until that stream is done with it."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream() without making an object
-    for t in allocated:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+def _current_stream(dev) -> int:
+    """Raw handle of the current stream (current_stream() without making an object).  The calls below that
+    take a stream run as under ``with torch.cuda.stream(stream)``: what they allocate is that stream's."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _dense(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
@@ -506,6 +502,9 @@ def _weight(weight, K: int, dev):
 def nvfp4_mx8_quantize(x: torch.Tensor, *, codes=None, scales=None, stream=None):
     """MXFP8-quantize x [M, K] (fp32 or bf16, K % 32 == 0).  Returns (codes u8 [M, K], scales u8 [M, K/32]):
     E4M3 codes (``codes.view(torch.float8_e4m3fn)`` reads them) under one E8M0 byte per 32 values."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_mx8_quantize(x, codes=codes, scales=scales)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     M, K = x.shape
@@ -518,7 +517,7 @@ def nvfp4_mx8_quantize(x: torch.Tensor, *, codes=None, scales=None, stream=None)
     st = lib().nvfp4_mx8_quantize(x.data_ptr(), _dtype_code(x.dtype), M, K, ld,
                                   _dense(codes, "codes", (M, K), torch.uint8, dev),
                                   _dense(scales, "scales", (M, K // 32), torch.uint8, dev),
-                                  _on_stream(dev, stream, codes, scales))
+                                  _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_mx8_quantize")
     return codes, scales
@@ -542,6 +541,10 @@ def nvfp4_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight:
     itself (fp32 or bf16); with fake_quantize the values its MXFP8 codes stand for.  With a residual, h
     is the sum, rounded to x's type (into the given h, which may be x or residual, or a new tensor);
     without one it is written only into a given h.  save_inv_rms: keep what the backward pass needs."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_rmsnorm(x, residual, weight, eps, mx8=mx8, y_dtype=y_dtype, fake_quantize=fake_quantize,
+                                 save_inv_rms=save_inv_rms, h=h)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     shape, dtype = x.shape, x.dtype
@@ -549,13 +552,12 @@ def nvfp4_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight:
     dev = _launch_device(x)
     ld_x = _pitch(x, "x", shape, dtype, dev)
     p_r = ld_r = p_h = ld_h = p_c = p_s = p_y = y_code = p_i = 0
-    new_h = codes = scales = y = inv_rms = None
+    codes = scales = y = inv_rms = None
     if residual is not None:
         ld_r, p_r = _pitch(residual, "residual", shape, dtype, dev), residual.data_ptr()
         if h is None:
-            h = new_h = torch.empty(M, K, dtype=dtype, device=dev)
-            ld_h, p_h = K, h.data_ptr()
-    if h is not None and new_h is None:
+            h = torch.empty(M, K, dtype=dtype, device=dev)
+    if h is not None:
         ld_h, p_h = _pitch(h, "h", shape, dtype, dev), h.data_ptr()
     p_w, w_code = _weight(weight, K, dev)
     if mx8:
@@ -572,7 +574,7 @@ def nvfp4_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight:
         p_i = inv_rms.data_ptr()
     st = lib().nvfp4_rmsnorm(x.data_ptr(), ld_x, p_r, ld_r, _dtype_code(dtype), M, K, p_w, w_code, eps, p_h, ld_h, p_c,
                              p_s, p_y, y_code, K, 1 if fake_quantize else 0, p_i,
-                             _on_stream(dev, stream, new_h, codes, scales, y, inv_rms))
+                             _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_rmsnorm")
     return RMSNormOutput(h, codes, scales, y, inv_rms)
@@ -588,6 +590,9 @@ def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, inv_rms: torch.Ten
     """Gradients of nvfp4_rmsnorm from dy (gradient of y), the forward's h (x where there was no residual)
     and inv_rms, and dh (gradient of h, or None).  Returns (dx, dw): dx [M, K] in h's type is the gradient
     of x and of residual; dw fp32 [K] is weight's (None with dweight=False)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_rmsnorm_backward(dy, h, inv_rms, weight, dh, dweight=dweight, dx=dx, workspace=workspace)
     if h.dim() != 2:
         raise ValueError("h must be 2-D")
     shape, dtype = h.shape, h.dtype
@@ -597,21 +602,21 @@ def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, inv_rms: torch.Ten
     ld_dh = 0 if dh is None else _pitch(dh, "dh", shape, dtype, dev)
     p_i = _dense(inv_rms, "inv_rms", (M,), torch.float32, dev)
     p_w, w_code = _weight(weight, K, dev)
-    new_dx = new_ws = dw = None
+    dw = None
     if dx is None:
-        dx = new_dx = torch.empty(M, K, dtype=dtype, device=dev)
+        dx = torch.empty(M, K, dtype=dtype, device=dev)
     ld_dx = _pitch(dx, "dx", shape, dtype, dev)
     p_dw = p_ws = ws_bytes = 0
     if dweight:
         dw = torch.empty(K, dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = new_ws = torch.empty(nvfp4_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(nvfp4_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
         elif workspace.device != dev:
             raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
         p_dw, p_ws, ws_bytes = dw.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = lib().nvfp4_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, 0 if dh is None else dh.data_ptr(), ld_dh,
                                       _dtype_code(dtype), M, K, p_w, w_code, p_i, dx.data_ptr(), ld_dx, p_dw, p_ws,
-                                      ws_bytes, _on_stream(dev, stream, new_dx, dw, new_ws))
+                                      ws_bytes, _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_rmsnorm_backward")
     return dx, dw
@@ -630,6 +635,7 @@ class _RMSNorm(torch.autograd.Function):
         return out.y.view(x.shape), None if residual is None else out.h.view(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         h, inv_rms, weight = ctx.saved_tensors
         want_dw = weight is not None and ctx.needs_input_grad[2]
@@ -660,6 +666,9 @@ def nvfp4_mx_gemm_w4a8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
                        out_dtype: torch.dtype = torch.bfloat16, *, out=None, stream=None) -> torch.Tensor:
     """Y = A B^T with A [M, K] MXFP8 (codes u8 [M, K], scales u8 [M, K/32]) and B [N, K] MXFP4 (packed u8
     [N, K/2], scales u8 [N, K/32]); all dense.  out: a tensor [M, N] (fp32 or bf16, unit stride along N)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_mx_gemm_w4a8(a, a_scales, b, b_scales, out_dtype, out=out)
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError("a and b must be 2-D")
     M, K = a.shape
@@ -668,12 +677,11 @@ def nvfp4_mx_gemm_w4a8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
     u8 = torch.uint8
     p_a, p_b = _dense(a, "a", (M, K), u8, dev), _dense(b, "b", (N, K // 2), u8, dev)
     p_as, p_bs = _dense(a_scales, "a_scales", (M, K // 32), u8, dev), _dense(b_scales, "b_scales", (N, K // 32), u8, dev)
-    new = None
     if out is None:
-        out = new = torch.empty(M, N, dtype=out_dtype, device=dev)
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
     ldc = _pitch(out, "out", (M, N), out.dtype, dev)
     st = lib().nvfp4_mx_gemm_w4a8(p_a, p_as, p_b, p_bs, M, N, K, out.data_ptr(), _dtype_code(out.dtype), ldc,
-                                  _on_stream(dev, stream, new))
+                                  _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_mx_gemm_w4a8")
     return out
@@ -691,6 +699,9 @@ def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_fre
     stride along D).  positions fp32 [T, axes]; axis_dims: how many leading elements of a head each axis
     turns; inv_freq fp32, one per pair (rope_inv_freq).  inverse: turn back (the gradient).  out: a
     tensor [T, H, D], x itself to turn in place, or None for a new dense one."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_rope_axes(x, positions, axis_dims, inv_freq, layout=layout, inverse=inverse, out=out)
     if x.dim() != 3:
         raise ValueError("x must be [T, H, D]")
     T, H, D = x.shape
@@ -698,9 +709,8 @@ def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_fre
     n = len(axis_dims)
     p_pos = _dense(positions, "positions", (T, n), torch.float32, dev)
     p_f = _dense(inv_freq, "inv_freq", (sum(axis_dims) // 2,), torch.float32, dev)
-    new = None
     if out is None:
-        out = new = torch.empty(T, H, D, dtype=x.dtype, device=dev)
+        out = torch.empty(T, H, D, dtype=x.dtype, device=dev)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
         raise ValueError("out must have x's shape, type and device")
     xt, xh, xd = x.stride()
@@ -709,7 +719,7 @@ def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_fre
         raise ValueError("x and out must have unit stride along D")
     st = lib().nvfp4_rope_axes(x.data_ptr(), _dtype_code(x.dtype), T, H, D, xt, xh, p_pos, n,
                                (ctypes.c_int32 * n)(*axis_dims), p_f, layout, 1 if inverse else 0, out.data_ptr(), yt, yh,
-                               _on_stream(dev, stream, new))
+                               _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_rope_axes")
     return out
@@ -723,6 +733,7 @@ class _RopeAxes(torch.autograd.Function):
         return nvfp4_rope_axes(x, positions, axis_dims, inv_freq, layout=layout)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         positions, inv_freq = ctx.saved_tensors
         axis_dims, layout = ctx.how

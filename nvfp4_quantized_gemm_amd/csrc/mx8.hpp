@@ -6,7 +6,8 @@
 // E4M3 exponent; the code is the E4M3 value nearest to v / X, ties to even, saturating at 448.
 // v * 2^(127 - b) is exact (a power of two; the result is below 512), so the hardware's
 // round-to-nearest-even conversion of it, clamped to 448 first (unclamped it gives NaN above 464),
-// is the code.  A block that holds an infinity or a NaN gets b = 255 (the E8M0 NaN) and zero codes.
+// is the code.  A block that holds an infinity or a NaN gets b = 255 (the E8M0 NaN) and NaN codes, so that
+// neither a dequantization nor a product turns it into numbers.
 #pragma once
 #include "common.hpp"
 
@@ -48,7 +49,7 @@ __device__ __forceinline__ uint32_t mx8_encode4(float a, float b, float c, float
 }
 // The 8 codes of a lane's values under scale byte b.
 __device__ __forceinline__ u32x2 mx8_encode8(const float (&v)[8], uint32_t b) {
-  if (b == 255u) return u32x2{0, 0};
+  if (b == 255u) return u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};
   const float m = mx8_inv_scale(b);
   return u32x2{mx8_encode4(v[0] * m, v[1] * m, v[2] * m, v[3] * m), mx8_encode4(v[4] * m, v[5] * m, v[6] * m, v[7] * m)};
 }

@@ -237,7 +237,7 @@ hipError_t launch_layout(const RopeArgs &a, int V, unsigned grid, size_t lds, hi
 // fp32, 38 MB: 20.1 us and 18.9).
 template <int DT>
 hipError_t launch_dtype(const RopeArgs &a, int V, unsigned grid, size_t lds, hipStream_t s) {
-  const bool stream = a.T * a.H * a.D * (DT == 0 ? 4 : 2) > (int64_t(128) << 20);
+  const bool stream = (int64_t)grid * a.tokens * a.H * a.D * (DT == 0 ? 4 : 2) > (int64_t(128) << 20);
   return stream ? launch_layout<DT, true>(a, V, grid, lds, s) : launch_layout<DT, false>(a, V, grid, lds, s);
 }
 
@@ -255,9 +255,18 @@ hipError_t launch_rope(RopeArgs a, hipStream_t s) {
   a.div_c = make_fastdiv((uint32_t)(a.halves ? a.D / (2 * V) : a.D / 8));
   a.div_h = make_fastdiv((uint32_t)a.H);
   a.div_p = make_fastdiv((uint32_t)(a.pairs > 0 ? a.pairs : 1));
-  const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
   const size_t lds = (size_t)tokens * a.pairs * sizeof(f32x2);
-  return a.dtype == 0 ? launch_dtype<0>(a, V, grid, lds, s) : launch_dtype<1>(a, V, grid, lds, s);
+  const int64_t es = a.dtype == 0 ? 4 : 2, most = tokens << 22;  // tokens of one launch's grid
+  for (int64_t left = a.T; left > 0; left -= most) {
+    a.T = left < most ? left : most;
+    const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
+    const hipError_t e = a.dtype == 0 ? launch_dtype<0>(a, V, grid, lds, s) : launch_dtype<1>(a, V, grid, lds, s);
+    if (e != hipSuccess) return e;
+    a.x = static_cast<const uint8_t *>(a.x) + a.T * a.ld_t * es;
+    a.y = static_cast<uint8_t *>(a.y) + a.T * a.ldy_t * es;
+    a.positions += a.T * a.n_axes;
+  }
+  return hipSuccess;
 }
 
 }  // namespace nvfp4

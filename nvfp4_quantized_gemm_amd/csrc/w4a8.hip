@@ -714,13 +714,15 @@ hipError_t launch_rows(const W4A8Args &g, hipStream_t s) {
 // compared by what their rounds cost.
 template <int OUT>
 hipError_t launch_out(const W4A8Args &g, hipStream_t s) {
-  if (256 * g.K >= (int64_t(1) << 31)) {  // the tiles' row offsets are 32 bits
+  auto tiles = [&](int64_t r, int64_t c) { return ((g.M + r - 1) / r) * ((g.N + c - 1) / c); };
+  // the tiles' row offsets are 32 bits, and their scale rows at least a word; the few-row kernel that takes
+  // shorter ones is launched over rows in y
+  if (256 * g.K >= (int64_t(1) << 31) || (g.K < 128 && (g.M > 32 * 65535 || tiles(32, 16) > (1 << 22)))) {
     int64_t grid = (g.M * g.N + 255) / 256;
     if (grid > 65536) grid = 65536;
     k_w4a8_generic<OUT><<<(unsigned)grid, 256, 0, s>>>(g.a, g.as, g.b, g.bs, g.M, g.N, g.K, g.c, g.ldc);
     return hipGetLastError();
   }
-  auto tiles = [&](int64_t r, int64_t c) { return ((g.M + r - 1) / r) * ((g.N + c - 1) / c); };
   const int64_t nk = (g.K + 127) / 128;
   // Few rows: up to about 192 blocks of 32 columns the kernel without staging is faster (one row, 4096 x
   // 4096: 4.9 us and 6.9; 16 rows: 6.6 and 7.0), above it the staged tile (16 rows, 8192 x 8192: 18.3 and

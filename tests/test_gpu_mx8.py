@@ -111,7 +111,7 @@ def test_quantize_non_finite_blocks_stay_apart():
         x[i, 40 + i] = bad
     codes, scales = nv.nvfp4_mx8_quantize(x.to(DEV))
     s = scales.cpu().numpy()
-    assert (s[:3, 1] == 255).all() and (codes.cpu()[:3, 32:64] == 0).all()
+    assert (s[:3, 1] == 255).all() and (codes.cpu()[:3, 32:64] == 0x7F).all()
     keep = np.ones((5, 4), bool)
     keep[:3, 1] = False
     assert np.array_equal(s[keep], clean_scales.cpu().numpy()[keep])
@@ -357,6 +357,46 @@ def test_w4a8_scale_blocks_and_positions():
         assert torch.equal(big, want.repeat(100, 1)), k
 
 
+@pytest.mark.parametrize("M", [3, 40, 200, 700])
+def test_w4a8_non_finite_rows_stay_apart(M):
+    """A row of the norm with a NaN or an infinity gives NaN in its own outputs only."""
+    N, K = 300, 1152
+    x = rnd(M, K, seed=M)
+    clean = nv.nvfp4_mx8_quantize(x.to(DEV))
+    _, _, b, sb = (t.to(DEV) for t in mx_operands(1, N, K, seed=4))
+    want = nv.nvfp4_mx_gemm_w4a8(*clean, b, sb, F32)
+    x[1, 1151], x[M - 1, 5] = float("nan"), float("-inf")
+    got = nv.nvfp4_mx_gemm_w4a8(*nv.nvfp4_mx8_quantize(x.to(DEV)), b, sb, F32)
+    bad = torch.zeros(M, dtype=torch.bool)
+    bad[1] = bad[M - 1] = True
+    assert torch.isnan(got.cpu()[bad]).all() and torch.equal(got.cpu()[~bad], want.cpu()[~bad])
+
+
+@pytest.mark.parametrize("M", [1, 24, 150, 600])
+@pytest.mark.parametrize("sa,sb", [(10, 200), (3, 240), (246, 12), (240, 100), (60, 60)])
+def test_w4a8_extreme_scales(M, sa, sb):
+    """Scales far from 1 on either side: widened operands down to bf16's subnormals and up to its largest exponents."""
+    N, K = 70, 160
+    a, _, b, _ = mx_operands(M, N, K, seed=6)
+    ops = (a, torch.full((M, K // 32), sa, dtype=torch.uint8), b, torch.full((N, K // 32), sb, dtype=torch.uint8))
+    y = nv.nvfp4_mx_gemm_w4a8(*[t.to(DEV) for t in ops], F32)
+    A, B = mx_values(*ops)
+    Y, R = A @ B.t(), A.abs() @ B.abs().t()
+    fits = R < 3e38
+    err = (y.cpu().double() - Y).abs()
+    assert (err <= 1e-5 * R + K * 2.0 ** -149)[fits].all()
+
+
+def test_w4a8_short_rows_of_scales():
+    """K below one scale word, many tiles."""
+    for M, N, K in ((1, 20000, 96), (5000, 300, 32), (3000, 3000, 64), (40000, 9000, 96)):
+        say("[w4a8 short K]", M, N, K)
+        ops = mx_operands(M, N, K, seed=7)
+        y = nv.nvfp4_mx_gemm_w4a8(*[t.to(DEV) for t in ops], F32)
+        for r in (slice(0, 70), slice(M - 70 if M > 70 else 0, M)):
+            check_product(y[r], *mx_values(ops[0][r], ops[1][r], *ops[2:]))
+
+
 def test_w4a8_rows_past_32_bits():
     """An activation of more than 4 GiB: its last rows and its first."""
     M, N, K = 140001, 40, 32768
@@ -444,6 +484,20 @@ def test_rope_strides_past_32_bits():
         y = nv.nvfp4_rope_axes(x, pos.to(DEV), (64,), nv.rope_inv_freq((64,)), layout=layout)
         want, tol = rope_ref(src, pos, (64,), nv.rope_inv_freq((64,), device="cpu"), layout == nv.ROPE_HALVES, False)
         assert ((y.cpu().double() - want).abs() <= tol + V * want.abs()).all()
+
+
+@pytest.mark.parametrize("layout", [nv.ROPE_PAIRS, nv.ROPE_HALVES])
+def test_rope_more_tokens_than_one_launch_takes(layout):
+    T = (16 << 22) + 37
+    x = torch.zeros(T, 1, 8, dtype=BF, device=DEV)
+    pos = torch.zeros(T, 1, device=DEV)
+    at = [0, 1, (16 << 22) - 1, 16 << 22, (16 << 22) + 20, T - 1]
+    src, p = rnd(len(at), 1, 8, seed=2, dtype=BF), torch.tensor([[1.0], [7.0], [30.0], [11.0], [5.0], [500.0]])
+    x[at], pos[at] = src.to(DEV), p.to(DEV)
+    y = nv.nvfp4_rope_axes(x, pos, (8,), nv.rope_inv_freq((8,)), layout=layout)
+    want, tol = rope_ref(src, p, (8,), nv.rope_inv_freq((8,), device="cpu"), layout == nv.ROPE_HALVES, False)
+    assert ((y[at].cpu().double() - want).abs() <= tol + V * want.abs()).all()
+    assert int((y != 0).any(2).sum()) == len(at)
 
 
 @pytest.mark.parametrize("layout", [nv.ROPE_PAIRS, nv.ROPE_HALVES])
