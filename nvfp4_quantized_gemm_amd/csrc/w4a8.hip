@@ -182,14 +182,15 @@ struct TileCfg {
   static constexpr int kG = WM * WN, kWaves = kG * KG, kThreads = 64 * kWaves;
   static constexpr int kTM = R / 32 / WM, kTN = C / 32 / WN;
   static constexpr int kA = R * 128, kB = C * 64, kStage = kA + kB;
-  static constexpr int kScaleWaves = (R + C + 63) / 64, kSlot = kScaleWaves * 1024;
+  static constexpr int kScaleUnits = (R + C + 63) / 64, kSlot = kScaleUnits * 1024;  // of 64 rows
+  static constexpr int kSU = (kScaleUnits + kG - 1) / kG;                            // per wave, at most
   static constexpr int kScales = S * kStage, kGroup = kScales + kSlots * kSlot, kLds = KG * kGroup;
   static constexpr int kNA = R / 8 / kG, kNB = C / 16 / kG, kDmas = kNA + kNB;  // DMAs per wave and chunk
   static constexpr int kPart = kTM * kTN * 4096;                               // a wave's sums
   static constexpr int kEpi = (KG - 1) * kG * kPart, kEpiWave = 32 * EpiPitch<C / WN, 4>::kPitch;
-  static constexpr int kWavesPerEu = (kLds <= 80 * 1024 ? 2 : 1) * kWaves / 4;
+  static constexpr int kWavesPerEu = ((kLds <= 80 * 1024 ? 2 : 1) * kWaves + 3) / 4;
   static_assert(kNA * kG == R / 8 && kNB * kG == C / 16, "even DMA split");
-  static_assert(kTM * WM * 32 == R && kTN * WN * 32 == C && kScaleWaves <= kG, "wave tiling");
+  static_assert(kTM * WM * 32 == R && kTN * WN * 32 == C, "wave tiling");
   static_assert(S >= 3 && S <= 8 && kLds <= 160 * 1024 && kEpi + kG * kEpiWave <= kLds, "LDS fits");
 };
 
@@ -260,42 +261,51 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
       g2l16((TAIL ? b_tile : b_tile + (int64_t)k * 64) + o, st + Cfg::kA + (wave + G * i) * 1024);
     }
   };
-  // all ones where this lane's block of step t of the run's chunk kc lies inside K, else 0
+  // all ones where this lane's block of step t of the run's chunk kc lies inside K, else 0 (SX = 16: the
+  // groups share the chunks evenly, as 4 divides their number and KG divides 4)
+  static_assert(4 % KG == 0, "even groups");
   auto inside = [&](int kc, int t) {
-    if constexpr (TAIL || KG > 1) return (k0 + kc) * 128 + 64 * t + 32 * lh < K ? ~0u : 0u;
+    if constexpr (TAIL || (KG > 1 && SX != 16)) return (k0 + kc) * 128 + 64 * t + 32 * lh < K ? ~0u : 0u;
     else return ~0u;
   };
 
-  // scales: row t of the group's threads is activation row t, then weight row t - R; block blk is the
+  // scales: unit u (wave u % G) is rows 64 u .. of the activation's, then the weight's; block blk is the
   // run's chunks 4 blk .. 4 blk + 3 (past the end: the last ones)
-  const bool scale_wave = Cfg::kScaleWaves == G || wave < Cfg::kScaleWaves;
-  const uint8_t *srow;
-  {
-    const int t = 64 * wave + lane;
-    srow = t < Cfg::kR ? as + (int64_t)min(m0 + t, M - 1) * nb
-                       : bs + (int64_t)min(n0 + min(t - Cfg::kR, Cfg::kC - 1), N - 1) * nb;
+  const uint8_t *srow[Cfg::kSU];
+#pragma unroll
+  for (int i = 0; i < Cfg::kSU; ++i) {
+    const int t = 64 * (wave + G * i) + lane;
+    srow[i] = t < Cfg::kR ? as + (int64_t)min(m0 + t, M - 1) * nb
+                          : bs + (int64_t)min(n0 + min(t - Cfg::kR, Cfg::kC - 1), N - 1) * nb;
   }
+  auto has_unit = [&](int i) { return Cfg::kScaleUnits % G == 0 || wave + G * i < Cfg::kScaleUnits; };
   uint8_t *const swave = ring + Cfg::kScales + wave * 1024;
-  u32x4 next_scales = {0, 0, 0, 0};
+  u32x4 next_scales[Cfg::kSU];
   auto issue_scales = [&](int blk, int slot) {
-    if (!scale_wave) return;
-    uint8_t *const at = swave + slot * Cfg::kSlot;
-    if constexpr (SX == 16) {
-      g2l16(srow + 16 * min(k0 / 4 + blk, nk / 4 - 1), at);
-    } else if constexpr (SX == 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) g2l4(srow + 4 * min(k0 + 4 * blk + i, nk - 1), at + 256 * i);
-    } else {
+    for (int i = 0; i < Cfg::kSU; ++i) {
+      if (!has_unit(i)) continue;
+      uint8_t *const at = swave + slot * Cfg::kSlot + i * (G * 1024);
+      if constexpr (SX == 16) {
+        g2l16(srow[i] + 16 * min(k0 / 4 + blk, nk / 4 - 1), at);
+      } else if constexpr (SX == 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) next_scales[i] = scale_word_raw(srow, min(k0 + 4 * blk + i, nk - 1), nb);
+        for (int w = 0; w < 4; ++w) g2l4(srow[i] + 4 * min(k0 + 4 * blk + w, nk - 1), at + 256 * w);
+      } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) next_scales[i][w] = scale_word_raw(srow[i], min(k0 + 4 * blk + w, nk - 1), nb);
+      }
     }
   };
   auto put_scales = [&](int blk, int slot) {  // SX = 1: the registers' words; the DMAs need no such step
     if constexpr (SX == 1) {
-      u32x4 v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = scale_word_shift(next_scales[i], min(k0 + 4 * blk + i, nk - 1), nb);
-      if (scale_wave) *reinterpret_cast<u32x4 *>(swave + slot * Cfg::kSlot + 16 * lane) = v;
+      for (int i = 0; i < Cfg::kSU; ++i) {
+        u32x4 v;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[w] = scale_word_shift(next_scales[i][w], min(k0 + 4 * blk + w, nk - 1), nb);
+        if (has_unit(i)) *reinterpret_cast<u32x4 *>(swave + slot * Cfg::kSlot + i * (G * 1024) + 16 * lane) = v;
+      }
     }
   };
 
@@ -336,6 +346,12 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
+  // All but the last n of this wave's DMAs have landed, and so have the other waves' of its ring; a wave
+  // with a ring of its own waits for nobody.
+  auto arrive = [&](auto n) {
+    if constexpr (G == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(n)::value) : "memory");
+    else wait_vmem_then_barrier<decltype(n)::value>();
+  };
 #pragma unroll
   for (int s = 0; s < Cfg::kSlots - 1; ++s) {
     issue_scales(s, s);
@@ -344,8 +360,8 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
 #pragma unroll
   for (int s = 0; s < S; ++s) issue(s, s, 0, Cfg::kDmas);
   put_scales(Cfg::kSlots - 2, Cfg::kSlots - 2);
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  wait_vmem_then_barrier<(S - 1) * Cfg::kDmas>();  // chunk 0 and scale block 0 are there
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0) alone
+  arrive(std::integral_constant<int, (S - 1) * Cfg::kDmas>{});  // chunk 0 and scale block 0 are there
   read_weight(0, 0);
   read_act(0, 0, 0);
   read_act(0, 0, 1);
@@ -387,7 +403,7 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
   }
   // one chunk; P = kc % 4 (compile time: the body is one basic block, which keeps the two steps'
   // products on their sides of the barrier)
-  constexpr int kScaleDmas = Cfg::kScaleWaves == G ? (SX == 16 ? 1 : 4) : 0;  // 0: not every wave has them
+  constexpr int kScaleDmas = Cfg::kScaleUnits % G == 0 ? Cfg::kSU * (SX == 16 ? 1 : 4) : 0;  // 0: not every wave has them
   int stage = 0, slot = 0;
   auto chunk = [&](int kc, auto phase) {
     constexpr int P = decltype(phase)::value;
@@ -411,7 +427,7 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
     // scale loads issued behind them) are still on their way
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0) alone
-    wait_vmem_then_barrier<(S - 2) * Cfg::kDmas + (P == 1 ? kScaleDmas : 0)>();
+    arrive(std::integral_constant<int, (S - 2) * Cfg::kDmas + (P == 1 ? kScaleDmas : 0)>{});
     __builtin_amdgcn_sched_barrier(0);
     uint32_t Na[TM], Nb[TN];
     if constexpr (P == 3) slot = slot == Cfg::kSlots - 1 ? 0 : slot + 1;
@@ -732,11 +748,16 @@ hipError_t launch_out(const W4A8Args &g, hipStream_t s) {
   if (g.M <= 16 && g.N <= 6144)
     return nk > 16 ? launch_rows<OUT, 16, 1, 1, 2>(g, s) : launch_rows<OUT, 8, 1, 1, 2>(g, s);
   if ((g.M <= 32 && g.N <= 2048 && nk <= 18) || g.K < 128) return launch_rows<OUT, 8, 2, 1, 2>(g, s);
-  if (tiles(32, 32) <= 256) return launch_tiles<OUT, TileCfg<32, 32, 1, 1, 4, 5>>(g, s);
+  // The 32 x 32 tile shares a CU with a second one (64 x 4608 x 1152, 288 tiles: 6.3 us and 6.5 with 64 x 32).
+  if (tiles(32, 32) <= 300) return launch_tiles<OUT, TileCfg<32, 32, 1, 1, 4, 3>>(g, s);
   if (tiles(64, 32) <= 256) return launch_tiles<OUT, TileCfg<64, 32, 2, 1, 4, 3>>(g, s);
-  if (tiles(64, 64) <= 256)  // short K: one group with a deeper ring (777 x 1001 x 2080: 12.0 us and 13.2)
-    return nk < 24 ? launch_tiles<OUT, TileCfg<64, 64, 2, 2, 1, 4>>(g, s) : launch_tiles<OUT, TileCfg<64, 64, 2, 2, 2, 3>>(g, s);
-  if (tiles(128, 64) <= 256) return launch_tiles<OUT, TileCfg<128, 64, 2, 2, 1, 3>>(g, s);
+  // Long K: a wave to 64 x 64, with half the conversions per product, in four or two groups (128 x 8192 x
+  // 8192: 21.7 us and 24.4; 256 x 8192 x 8192: 34.6 and 41.3); short K: more waves on the tile (256 x 4096 x
+  // 4096: 13.6 us and 14.0; 512 x 4608 x 1152: 12.2 and 16.6).
+  if (tiles(64, 64) <= 256)
+    return nk >= 48 ? launch_tiles<OUT, TileCfg<64, 64, 1, 1, 4, 3>>(g, s) : launch_tiles<OUT, TileCfg<64, 64, 2, 2, 2, 3>>(g, s);
+  if (tiles(128, 64) <= 256)
+    return nk >= 24 ? launch_tiles<OUT, TileCfg<128, 64, 2, 1, 2, 3>>(g, s) : launch_tiles<OUT, TileCfg<128, 64, 2, 2, 1, 3>>(g, s);
   const double small = 0.29 / 256 * (double)tiles(128, 128), big = (double)((tiles(256, 256) + 255) / 256);
   return small <= big ? launch_tiles<OUT, TileCfg<128, 128, 2, 2, 1, 3>>(g, s)
                       : launch_tiles<OUT, TileCfg<256, 256, 2, 4, 1, 3>>(g, s);
