@@ -104,9 +104,11 @@ namespace {
 
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
-// A scale byte as the float the conversions take (they read its exponent field).
-__device__ __forceinline__ float scale_of(uint32_t word, int byte) {
-  return __uint_as_float(((word >> (8 * byte)) & 255u) << 23);
+// Byte i of a word of scale bytes as the float the conversions take: they read its exponent field alone
+// (checked over random other bits), so turning the byte there is all.  turn = scale_turn(i).
+__device__ __forceinline__ uint32_t scale_turn(int i) { return (8 * i + 9) & 31; }
+__device__ __forceinline__ float scale_at(uint32_t word, uint32_t turn) {
+  return __uint_as_float(__builtin_amdgcn_alignbit(word, word, turn));
 }
 // 8 E4M3 codes of words lo, hi, or the 8 E2M1 codes of a word, times their scale: exact in bf16.
 __device__ __forceinline__ bf16x8 widen_act(uint32_t lo, uint32_t hi, float X) {
@@ -369,11 +371,12 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
 
   // Operands of 8 k's (a quarter of a step), widened.  Step t: lane (r, h) takes block 2 t + h.
   bf16x8 wa[TM], wb[2][TN];
+  const uint32_t turn[2] = {scale_turn(lh), scale_turn(2 + lh)};
   auto widen_a = [&](int t, int u, int i, uint32_t word) {
-    wa[i] = widen_act(Af[i][u >> 1][2 * (u & 1)], Af[i][u >> 1][2 * (u & 1) + 1], scale_of(word >> (8 * lh), 2 * t));
+    wa[i] = widen_act(Af[i][u >> 1][2 * (u & 1)], Af[i][u >> 1][2 * (u & 1) + 1], scale_at(word, turn[t]));
   };
   auto widen_b = [&](int t, int u, int j, uint32_t word, uint32_t mask) {
-    wb[u & 1][j] = widen_weight(Bf[t][j][u] & mask, scale_of(word >> (8 * lh), 2 * t));
+    wb[u & 1][j] = widen_weight(Bf[t][j][u] & mask, scale_at(word, turn[t]));
   };
   // The products of substep u, and behind those that use it last each operand of the next (t, v)
   auto substep = [&](int u, int t, int v, const uint32_t (&sa)[TM], const uint32_t (&sb)[TN], uint32_t mask) {
@@ -603,14 +606,15 @@ __global__ __launch_bounds__(64 * W) void k_w4a8_rows(const uint8_t *__restrict_
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  const uint32_t turn = scale_turn(q);
   auto multiply = [&](const Run &f) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float Xa[MT], Xb[NT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) Xa[i] = scale_of(f.sa[i][u] >> (8 * q), 0);
+      for (int i = 0; i < MT; ++i) Xa[i] = scale_at(f.sa[i][u], turn);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) Xb[j] = scale_of(f.sb[j][u] >> (8 * q), 0);
+      for (int j = 0; j < NT; ++j) Xb[j] = scale_at(f.sb[j][u], turn);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         bf16x8 wb[NT], wa[MT];
