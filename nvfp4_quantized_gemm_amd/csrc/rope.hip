@@ -10,6 +10,10 @@
 // cos and sin are taken once per token and pair, into LDS, for all heads.  The angle is brought to
 // turns with 1/(2 pi) held in two floats, so the reduction is exact to 2^-48 of the angle and
 // large positions lose nothing beyond the angle's own fp32 rounding.
+//
+// Bound by memory: every element is read and written once.  10240 x 64 x 128 bf16 out of a QKV row (pairs): 56.6
+// us, 5.9 TB/s, the rate of a large copy; halves of 64: 63.6 us; 4097 x 32 x 72 (38 MB): pairs 10.1 us, halves of
+// 18 (4-byte accesses) 12.9 us, one token 2.9 us, where the launch and one round of latency count.
 #include <type_traits>
 
 #include "launch.hpp"

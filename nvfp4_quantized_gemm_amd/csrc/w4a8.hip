@@ -88,10 +88,11 @@ __global__ __launch_bounds__(256) void k_w4a8_generic(const uint8_t *__restrict_
 //   activation [R rows][8 pieces]   weight [C rows][4 pieces]
 // A DMA copies 8 activation rows' 128 bytes or 16 weight rows' 64, neighbouring lanes neighbouring pieces
 // (with rows in neighbouring lanes each lane is a request of its own, and the address unit was what bound
-// every tile size: 64 x 8192 x 8192 took 28 us, .. now).  Piece p of row r lies in slot p ^ (r / 2 % 8), or
-// p ^ (r / 4 % 4) of a weight row, so that the 16 rows of a read pass lie in 16 different bank groups.  Scales: [2 slots][R + C rows], blocks of 4 chunks (16 bytes of a
-// row), one row per thread: a 16-byte DMA lane, four 4-byte ones ([64 rows' chunk 0][chunk 1]..), or, where
-// rows of scales are not aligned, registers that are written to LDS two chunks later.
+// every tile size: 64 x 8192 x 8192 took 28 us, and 16 with this).  Piece p of row r lies in slot
+// p ^ (r / 2 % 8), or p ^ (r / 4 % 4) of a weight row, so that the 16 rows of a read pass lie in 16
+// different bank groups.  Scales: blocks of 4 chunks (16 bytes of a row) in two slots, one row per lane: a
+// 16-byte DMA lane, four 4-byte ones ([64 rows' chunk 0][chunk 1]..), or, where rows of scales are not
+// aligned, registers that are written to LDS two chunks later.
 //
 // A chunk is two 64-k steps.  While step 0 multiplies, step 1's operands are read; in the middle one
 // barrier says that the next chunk has landed everywhere and that this one's stage is free, the DMA of
@@ -99,6 +100,11 @@ __global__ __launch_bounds__(256) void k_w4a8_generic(const uint8_t *__restrict_
 // Rows past M or N repeat the last one and are never stored.  Past K (the end of the last chunk where K is
 // no multiple of 128, and the chunks that a short group has too many) pieces are read from inside the row
 // and the weight's words masked to zero: products with finite codes are then 0.
+//
+// Measured: 8192^3 in 0.74 to 0.77 ms, 1.43 to 1.49 PFLOP/s (a bf16 torch.matmul of that size: 1.30), bound by
+// power: 76 % of the cycles in the matrix cores at 1.88 GHz.  With few tiles a 128 x 128 workgroup alone on
+// its CU keeps them 62 % busy: a chunk is about 260 instructions a wave, 4 clocks each, beside 1024 clocks of
+// products, and two workgroups on a CU (or two groups of one) get little more out of it.
 
 namespace {
 
@@ -406,7 +412,9 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
   }
   // one chunk; P = kc % 4 (compile time: the body is one basic block, which keeps the two steps'
   // products on their sides of the barrier)
-  constexpr int kScaleDmas = Cfg::kScaleUnits % G == 0 ? Cfg::kSU * (SX == 16 ? 1 : 4) : 0;  // 0: not every wave has them
+  // scale DMAs that may stay in flight in phase 1; none where not every wave has them, or where they are plain
+  // loads, whose number is the compiler's
+  constexpr int kScaleDmas = Cfg::kScaleUnits % G == 0 && SX != 1 ? Cfg::kSU * (SX == 16 ? 1 : 4) : 0;
   int stage = 0, slot = 0;
   auto chunk = [&](int kc, auto phase) {
     constexpr int P = decltype(phase)::value;
@@ -514,8 +522,10 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
 
 // ---- few rows -----------------------------------------------------------------------------------------
 //
-// A workgroup owns 16 NT output columns and up to 16 MT rows; its W waves take every W-th run of U 128-k chunks and
-// their sums are added in LDS in wave order.  Operands straight from memory: lane (r, q) = (l % 16, l / 16)
+// Bound by latency: the weight is read once, 17/32 B a value, and there are few bytes to a CU (4608 x 1152
+// for one row: 3.2 us, 2.0 of them the launch and 2.06 a bare read of the weight; 4096 x 4096: 4.9 us).
+// A workgroup owns 16 NT output columns and up to 16 MT rows; its W waves take every W-th run of U 128-k
+// chunks and their sums are added in LDS in the order of the runs.  Operands straight from memory: lane (r, q) = (l % 16, l / 16)
 // takes block q of row r, and its 32 values make four v_mfma_f32_16x16x32_bf16 of 8 k from every block.
 // A weight load covers 64 contiguous bytes of 16 rows.  U chunks' loads are in flight while the U before
 // them multiply.
