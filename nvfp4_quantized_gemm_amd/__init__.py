@@ -456,34 +456,40 @@ def nvfp4_mx_gemm(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sc
 ROPE_PAIRS, ROPE_HALVES = 0, 1
 
 
-def _launch_device(ref: torch.Tensor):
-    """ref's device, which must be the current one (the library launches there)."""
-    dev = ref.device
-    if dev.type != "cuda":
+_u8, _f32 = torch.uint8, torch.float32
+
+
+# The checks below run on every call, also where the call is one token's and takes as long as its launch, so
+# they are few and plain: get_device() and `is` instead of comparing device and type objects, one condition
+# for all operands of a kind, and the explanation only once something is wrong.
+
+def _launch_device(ref: torch.Tensor) -> int:
+    """Index of ref's device, which must be the current one (the library launches there)."""
+    i = ref.get_device()
+    if i < 0:
         raise ValueError("the operands must be device tensors")
-    if dev.index != torch._C._cuda_getDevice():
-        raise ValueError(f"the operands are on {dev}, which is not the current device")
-    return dev
+    if i != torch._C._cuda_getDevice():
+        raise ValueError(f"the operands are on {ref.device}, which is not the current device")
+    return i
 
 
-def _current_stream(dev) -> int:
-    """Raw handle of the current stream (current_stream() without making an object).  The calls below that
-    take a stream run as under ``with torch.cuda.stream(stream)``: what they allocate is that stream's."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+# Raw handle of the current stream of a device (current_stream() without making an object).  The calls below
+# that take a stream run as under ``with torch.cuda.stream(stream)``: what they allocate is that stream's.
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _dense(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
+def _dense(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
     """Address of a dense tensor of the given shape (a tuple), type and device."""
-    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _pitch(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
+def _pitch(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
     """Row pitch (elements) of a matrix of the given shape, type and device with unit stride along K."""
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     if t.is_contiguous():
         return shape[1]
     ld, step = t.stride()
@@ -492,7 +498,7 @@ def _pitch(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
     return ld if shape[0] > 1 else shape[1]
 
 
-def _weight(weight, K: int, dev):
+def _weight(weight, K: int, dev: int):
     """(address, dtype code) of an optional weight vector."""
     if weight is None:
         return 0, 0
@@ -509,14 +515,16 @@ def nvfp4_mx8_quantize(x: torch.Tensor, *, codes=None, scales=None, stream=None)
         raise ValueError("x must be 2-D")
     M, K = x.shape
     dev = _launch_device(x)
-    ld = _pitch(x, "x", x.shape, x.dtype, dev)
+    ld = K if x.is_contiguous() else _pitch(x, "x", x.shape, x.dtype, dev)
     if codes is None:
-        codes = torch.empty(M, K, dtype=torch.uint8, device=dev)
+        codes = torch.empty(M, K, dtype=_u8, device=x.device)
+    else:
+        _dense(codes, "codes", (M, K), _u8, dev)
     if scales is None:
-        scales = torch.empty(M, K // 32, dtype=torch.uint8, device=dev)
-    st = lib().nvfp4_mx8_quantize(x.data_ptr(), _dtype_code(x.dtype), M, K, ld,
-                                  _dense(codes, "codes", (M, K), torch.uint8, dev),
-                                  _dense(scales, "scales", (M, K // 32), torch.uint8, dev),
+        scales = torch.empty(M, K // 32, dtype=_u8, device=x.device)
+    else:
+        _dense(scales, "scales", (M, K // 32), _u8, dev)
+    st = lib().nvfp4_mx8_quantize(x.data_ptr(), _dtype_code(x.dtype), M, K, ld, codes.data_ptr(), scales.data_ptr(),
                                   _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_mx8_quantize")
@@ -547,34 +555,35 @@ def nvfp4_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight:
                                  save_inv_rms=save_inv_rms, h=h)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
-    shape, dtype = x.shape, x.dtype
+    shape, dtype, device = x.shape, x.dtype, x.device
     M, K = shape
     dev = _launch_device(x)
-    ld_x = _pitch(x, "x", shape, dtype, dev)
-    p_r = ld_r = p_h = ld_h = p_c = p_s = p_y = y_code = p_i = 0
+    ld_x = K if x.is_contiguous() else _pitch(x, "x", shape, dtype, dev)
+    p_r = ld_r = p_h = ld_h = p_w = w_code = p_c = p_s = p_y = y_code = p_i = 0
     codes = scales = y = inv_rms = None
     if residual is not None:
         ld_r, p_r = _pitch(residual, "residual", shape, dtype, dev), residual.data_ptr()
         if h is None:
-            h = torch.empty(M, K, dtype=dtype, device=dev)
-    if h is not None:
+            h = torch.empty(M, K, dtype=dtype, device=device)
+            ld_h, p_h = K, h.data_ptr()
+    if h is not None and not p_h:
         ld_h, p_h = _pitch(h, "h", shape, dtype, dev), h.data_ptr()
-    p_w, w_code = _weight(weight, K, dev)
+    if weight is not None:
+        p_w, w_code = _weight(weight, K, dev)
     if mx8:
-        codes = torch.empty(M, K, dtype=torch.uint8, device=dev)
-        scales = torch.empty(M, K // 32, dtype=torch.uint8, device=dev)
+        codes = torch.empty(M, K, dtype=_u8, device=device)
+        scales = torch.empty(M, K // 32, dtype=_u8, device=device)
         p_c, p_s = codes.data_ptr(), scales.data_ptr()
     if y_dtype is not None:
-        y = torch.empty(M, K, dtype=y_dtype, device=dev)
+        y = torch.empty(M, K, dtype=y_dtype, device=device)
         p_y, y_code = y.data_ptr(), _dtype_code(y_dtype)
     elif fake_quantize:
         raise ValueError("fake_quantize needs y_dtype")
     if save_inv_rms:
-        inv_rms = torch.empty(M, dtype=torch.float32, device=dev)
+        inv_rms = torch.empty(M, dtype=_f32, device=device)
         p_i = inv_rms.data_ptr()
     st = lib().nvfp4_rmsnorm(x.data_ptr(), ld_x, p_r, ld_r, _dtype_code(dtype), M, K, p_w, w_code, eps, p_h, ld_h, p_c,
-                             p_s, p_y, y_code, K, 1 if fake_quantize else 0, p_i,
-                             _current_stream(dev))
+                             p_s, p_y, y_code, K, 1 if fake_quantize else 0, p_i, _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_rmsnorm")
     return RMSNormOutput(h, codes, scales, y, inv_rms)
@@ -595,28 +604,34 @@ def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, inv_rms: torch.Ten
             return nvfp4_rmsnorm_backward(dy, h, inv_rms, weight, dh, dweight=dweight, dx=dx, workspace=workspace)
     if h.dim() != 2:
         raise ValueError("h must be 2-D")
-    shape, dtype = h.shape, h.dtype
+    shape, dtype, device = h.shape, h.dtype, h.device
     M, K = shape
     dev = _launch_device(h)
-    ld_h, ld_dy = _pitch(h, "h", shape, dtype, dev), _pitch(dy, "dy", shape, dtype, dev)
-    ld_dh = 0 if dh is None else _pitch(dh, "dh", shape, dtype, dev)
-    p_i = _dense(inv_rms, "inv_rms", (M,), torch.float32, dev)
+    ld_h = K if h.is_contiguous() else _pitch(h, "h", shape, dtype, dev)
+    ld_dy = _pitch(dy, "dy", shape, dtype, dev)
+    p_dh = ld_dh = p_dw = p_ws = ws_bytes = 0
+    if dh is not None:
+        ld_dh, p_dh = _pitch(dh, "dh", shape, dtype, dev), dh.data_ptr()
+    p_i = _dense(inv_rms, "inv_rms", (M,), _f32, dev)
     p_w, w_code = _weight(weight, K, dev)
-    dw = None
     if dx is None:
-        dx = torch.empty(M, K, dtype=dtype, device=dev)
-    ld_dx = _pitch(dx, "dx", shape, dtype, dev)
-    p_dw = p_ws = ws_bytes = 0
+        dx, ld_dx = torch.empty(M, K, dtype=dtype, device=device), K
+    else:
+        ld_dx = _pitch(dx, "dx", shape, dtype, dev)
+    L = lib()
+    dw = None
     if dweight:
-        dw = torch.empty(K, dtype=torch.float32, device=dev)
+        dw = torch.empty(K, dtype=_f32, device=device)
         if workspace is None:
-            workspace = torch.empty(nvfp4_rmsnorm_backward_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev:
-            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
-        p_dw, p_ws, ws_bytes = dw.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = lib().nvfp4_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, 0 if dh is None else dh.data_ptr(), ld_dh,
-                                      _dtype_code(dtype), M, K, p_w, w_code, p_i, dx.data_ptr(), ld_dx, p_dw, p_ws,
-                                      ws_bytes, _current_stream(dev))
+            ws_bytes = L.nvfp4_rmsnorm_backward_workspace_bytes(M, K)
+            workspace = torch.empty(ws_bytes, dtype=_u8, device=device)
+        elif workspace.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
+        p_dw, p_ws = dw.data_ptr(), workspace.data_ptr()
+    st = L.nvfp4_rmsnorm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, p_dh, ld_dh, _dtype_code(dtype), M, K, p_w,
+                                  w_code, p_i, dx.data_ptr(), ld_dx, p_dw, p_ws, ws_bytes, _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_rmsnorm_backward")
     return dx, dw
@@ -674,14 +689,21 @@ def nvfp4_mx_gemm_w4a8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
     M, K = a.shape
     N = b.shape[0]
     dev = _launch_device(a)
-    u8 = torch.uint8
-    p_a, p_b = _dense(a, "a", (M, K), u8, dev), _dense(b, "b", (N, K // 2), u8, dev)
-    p_as, p_bs = _dense(a_scales, "a_scales", (M, K // 32), u8, dev), _dense(b_scales, "b_scales", (N, K // 32), u8, dev)
+    if not (a.dtype is _u8 and a.is_contiguous()
+            and b.dtype is _u8 and b.is_contiguous() and b.shape[1] == K // 2 and b.get_device() == dev
+            and a_scales.dtype is _u8 and a_scales.is_contiguous() and a_scales.shape == (M, K // 32)
+            and b_scales.dtype is _u8 and b_scales.is_contiguous() and b_scales.shape == (N, K // 32)
+            and a_scales.get_device() == dev and b_scales.get_device() == dev):
+        _dense(a, "a", (M, K), _u8, dev)
+        _dense(a_scales, "a_scales", (M, K // 32), _u8, dev)
+        _dense(b, "b", (N, K // 2), _u8, dev)
+        _dense(b_scales, "b_scales", (N, K // 32), _u8, dev)
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype, device=dev)
-    ldc = _pitch(out, "out", (M, N), out.dtype, dev)
-    st = lib().nvfp4_mx_gemm_w4a8(p_a, p_as, p_b, p_bs, M, N, K, out.data_ptr(), _dtype_code(out.dtype), ldc,
-                                  _current_stream(dev))
+        out, ldc = torch.empty(M, N, dtype=out_dtype, device=a.device), N
+    else:
+        ldc = _pitch(out, "out", (M, N), out.dtype, dev)
+    st = lib().nvfp4_mx_gemm_w4a8(a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, N, K,
+                                  out.data_ptr(), _dtype_code(out.dtype), ldc, _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_mx_gemm_w4a8")
     return out
@@ -707,14 +729,16 @@ def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_fre
     T, H, D = x.shape
     dev = _launch_device(x)
     n = len(axis_dims)
-    p_pos = _dense(positions, "positions", (T, n), torch.float32, dev)
-    p_f = _dense(inv_freq, "inv_freq", (sum(axis_dims) // 2,), torch.float32, dev)
-    if out is None:
-        out = torch.empty(T, H, D, dtype=x.dtype, device=dev)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
-        raise ValueError("out must have x's shape, type and device")
+    p_pos = _dense(positions, "positions", (T, n), _f32, dev)
+    p_f = _dense(inv_freq, "inv_freq", (sum(axis_dims) // 2,), _f32, dev)
     xt, xh, xd = x.stride()
-    yt, yh, yd = out.stride()
+    if out is None:
+        out = torch.empty(T, H, D, dtype=x.dtype, device=x.device)
+        yt, yh, yd = H * D, D, 1
+    elif out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != dev:
+        raise ValueError("out must have x's shape, type and device")
+    else:
+        yt, yh, yd = out.stride()
     if xd != 1 or yd != 1:
         raise ValueError("x and out must have unit stride along D")
     st = lib().nvfp4_rope_axes(x.data_ptr(), _dtype_code(x.dtype), T, H, D, xt, xh, p_pos, n,
