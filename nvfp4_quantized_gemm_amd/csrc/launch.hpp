@@ -173,7 +173,7 @@ struct RopeArgs {  // rope.hip
   int H, D, n_axes, pairs, halves, inverse;
   int pair_end[kRopeMaxAxes];  // pairs of the axes up to and with this one
   const float *positions, *inv_freq;
-  int tokens = 0;  // per workgroup; the launcher sets this and the divisors
+  int tokens = 0, heads = 0, chunks = 0;  // per workgroup; the launcher sets these and the divisors
   FastDiv div_c{}, div_h{}, div_p{};
 };
 hipError_t launch_rope(RopeArgs a, hipStream_t stream);

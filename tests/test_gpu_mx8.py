@@ -428,7 +428,10 @@ def rope_ref(x, pos, dims, f, halves, inverse):
 
 ROPE = [(1, 1, 8, (8,)), (1, 32, 72, (24, 24, 24)), (2, 3, 64, (64,)), (5, 7, 72, (36, 36)), (67, 5, 128, (44, 42, 42)),
         (33, 12, 128, (16, 56, 56)), (9, 2, 96, (30, 20)), (3, 1, 1024, (512, 256, 128, 100)), (130, 40, 80, (80,)),
-        (17, 3, 104, (2, 0, 50)), (4, 2, 16, (0,)), (6, 140, 64, (32, 16, 16))]
+        (17, 3, 104, (2, 0, 50)), (4, 2, 16, (0,)), (6, 140, 64, (32, 16, 16)),
+        # heads in chunks, the last one shorter; many tokens of few heads; sections of one and two pairs
+        (3, 57, 200, (66, 66, 66)), (2, 17, 1024, (20, 2, 1000)), (9000, 1, 40, (20, 20)), (5003, 2, 24, (4, 6, 14)),
+        (2, 40007, 8, (8,)), (700, 32, 72, (24, 24, 24)), (8201, 3, 16, (2, 4, 6, 2))]
 
 
 @pytest.mark.parametrize("T,H,D,dims", ROPE)
