@@ -663,17 +663,20 @@ class _RMSNorm(torch.autograd.Function):
 
 
 def _rows_of(t: torch.Tensor) -> torch.Tensor:
-    """t [..., K] as a matrix of rows of K that the kernels take (copied only where its layout needs it)."""
+    """t [..., K] as a matrix of rows of K that the kernels take (copied only where its layout needs it: a gradient
+    that autograd has expanded, rows that overlap, memory off 16 bytes)."""
     m = t.reshape(-1, t.shape[-1])
-    es = t.element_size()
-    return m if m.stride(1) == 1 and m.stride(0) * es % 16 == 0 and m.data_ptr() % 16 == 0 else m.contiguous()
+    rows, K = m.shape
+    pitched = m.stride(1) == 1 and (rows <= 1 or (m.stride(0) >= K and m.stride(0) * t.element_size() % 16 == 0))
+    # clone, not contiguous(): that returns a dense tensor as it is, wherever it lies
+    return m if pitched and m.data_ptr() % 16 == 0 else m.clone(memory_format=torch.contiguous_format)
 
 
 def rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
             eps: float = 1e-6, fake_quantize: bool = False):
     """Differentiable RMS norm with the residual's addition over the last dimension: (y, h) with h the sum
-    (None without a residual).  fake_quantize: y holds the values of its MXFP8 codes, with a
-    straight-through gradient (quantization-aware training)."""
+    (None without a residual), of tensors in any strides.  fake_quantize: y holds the values of its MXFP8 codes,
+    with a straight-through gradient (quantization-aware training)."""
     return _RMSNorm.apply(x, residual, weight, eps, fake_quantize)
 
 
@@ -749,25 +752,33 @@ def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_fre
     return out
 
 
+def _heads_of(t: torch.Tensor) -> torch.Tensor:
+    """t [T, H, D] in a layout that the rotation reads (copied only where its own needs it)."""
+    es = t.element_size()
+    taken = t.dim() != 3 or (t.stride(2) == 1 and t.data_ptr() % 16 == 0
+                             and t.stride(0) * es % 16 == 0 and t.stride(1) * es % 16 == 0)
+    return t if taken else t.clone(memory_format=torch.contiguous_format)
+
+
 class _RopeAxes(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, positions, axis_dims, inv_freq, layout):
         ctx.save_for_backward(positions, inv_freq)
         ctx.how = (axis_dims, layout)
-        return nvfp4_rope_axes(x, positions, axis_dims, inv_freq, layout=layout)
+        return nvfp4_rope_axes(_heads_of(x), positions, axis_dims, inv_freq, layout=layout)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         positions, inv_freq = ctx.saved_tensors
         axis_dims, layout = ctx.how
-        dx = nvfp4_rope_axes(dy.contiguous(), positions, axis_dims, inv_freq, layout=layout, inverse=True)
+        dx = nvfp4_rope_axes(_heads_of(dy), positions, axis_dims, inv_freq, layout=layout, inverse=True)
         return dx, None, None, None, None
 
 
 def rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_freq: torch.Tensor,
               layout: int = ROPE_PAIRS) -> torch.Tensor:
-    """Differentiable nvfp4_rope_axes (the gradient of x is the inverse rotation)."""
+    """Differentiable nvfp4_rope_axes of x in any strides (the gradient of x is the inverse rotation)."""
     return _RopeAxes.apply(x, positions, tuple(axis_dims), inv_freq, layout)
 
 
