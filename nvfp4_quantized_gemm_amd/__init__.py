@@ -642,6 +642,8 @@ class _RMSNorm(torch.autograd.Function):
     def forward(ctx, x, residual, weight, eps, fake_quantize):
         ctx.set_materialize_grads(False)
         x2 = _rows_of(x)
+        if weight is not None and not (weight.is_contiguous() and weight.data_ptr() % 16 == 0):
+            weight = weight.clone(memory_format=torch.contiguous_format)  # a slice of a flat buffer, an expanded scalar
         out = nvfp4_rmsnorm(x2, None if residual is None else _rows_of(residual), weight, eps, mx8=False,
                             y_dtype=x.dtype, fake_quantize=fake_quantize, save_inv_rms=True)
         ctx.save_for_backward(x2 if residual is None else out.h, out.inv_rms, weight)

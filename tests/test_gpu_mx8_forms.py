@@ -54,6 +54,20 @@ def test_rmsnorm_under_sums_over_tokens_and_behind_other_values(dtype):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("form", ["off 16 bytes", "expanded", "strided"])
+def test_rmsnorm_weight(dtype, form):
+    M, K = 7, 96
+    w = {"off 16 bytes": lambda t: off16(t), "expanded": lambda t: t[:1].expand(K),
+         "strided": lambda t: t.repeat_interleave(2)[::2]}[form](1 + 0.1 * rnd(K, seed=5, dtype=dtype))
+    x, dy = rnd(M, K, seed=1, dtype=dtype), rnd(M, K, seed=2, dtype=dtype)
+    xs, ws, wd = (t.detach().requires_grad_() for t in (x, w, w.clone(memory_format=torch.contiguous_format)))
+    y, want = nv.rmsnorm(xs, None, ws)[0], nv.rmsnorm(xs, None, wd)[0]
+    assert torch.equal(y, want)
+    for a, b in zip(torch.autograd.grad(y, (xs, ws), dy), torch.autograd.grad(want, (xs, wd), dy)):
+        assert torch.equal(a, b)
+
+
 HEADS = {"dense": lambda t: t, "expanded heads": lambda t: t[:, :1].expand(t.shape), "off 16 bytes": off16,
          "expanded tokens": lambda t: t[:1].expand(t.shape), "heads first": lambda t: t.transpose(0, 1).contiguous().transpose(0, 1),
          "strided": lambda t: t.repeat_interleave(2, 2)[..., ::2],

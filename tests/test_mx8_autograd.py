@@ -103,6 +103,21 @@ def test_rmsnorm_takes_every_gradient_and_input(name, form):
         assert torch.allclose(got, want, rtol=1e-4, atol=1e-5 * float(want.abs().max()))
 
 
+@pytest.mark.parametrize("form", ["offset", "expanded", "strided"])
+def test_rmsnorm_takes_every_weight(form):
+    K = 64
+    torch.manual_seed(2)
+    x = torch.randn(3, K)
+    leaf = {"offset": torch.rand(K + 1), "expanded": torch.rand(1), "strided": torch.rand(2 * K)}[form].requires_grad_()
+    w = {"offset": lambda: leaf[1:], "expanded": lambda: leaf.expand(K), "strided": lambda: leaf[::2]}[form]
+    grads = []
+    for f in (lambda: nv.rmsnorm(x, None, w(), EPS)[0], lambda: reference(x, None, w())[0]):
+        f().square().sum().backward()
+        grads.append(leaf.grad)
+        leaf.grad = None
+    assert torch.allclose(*grads, rtol=1e-4, atol=1e-5 * float(grads[1].abs().max()))
+
+
 @pytest.mark.parametrize("form", ["dense", "expanded", "offset", "strided", "odd pitch", "heads first"])
 def test_rope_takes_every_gradient_and_input(form):
     T, H, D, dims = 3, 4, 16, (8, 4)
