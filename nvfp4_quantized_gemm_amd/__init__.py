@@ -746,6 +746,10 @@ def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_fre
         yt, yh, yd = out.stride()
     if xd != 1 or yd != 1:
         raise ValueError("x and out must have unit stride along D")
+    if T == 1:  # the pitch of a single token or head is never used, whatever it is
+        xt = yt = 0
+    if H == 1:
+        xh = yh = 0
     st = lib().nvfp4_rope_axes(x.data_ptr(), _dtype_code(x.dtype), T, H, D, xt, xh, p_pos, n,
                                (ctypes.c_int32 * n)(*axis_dims), p_f, layout, 1 if inverse else 0, out.data_ptr(), yt, yh,
                                _current_stream(dev))

@@ -88,3 +88,18 @@ def test_rope(T, H, dtype, layout, form):
     assert torch.equal(y, nv.nvfp4_rope_axes(dense[0], pos, dims, f, layout=layout))
     dx, = torch.autograd.grad(y, xs, dy)
     assert torch.equal(dx, nv.nvfp4_rope_axes(dense[1], pos, dims, f, layout=layout, inverse=True))
+
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 5), (6, 1)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rope_of_one_token_or_one_head_at_any_pitch(T, H, dtype):
+    """The pitch of a dimension of one element is never used, whatever it is."""
+    D, dims, odd = 72, (24, 20, 16), 72 * H * T + 13
+    x = rnd(T, H, D, seed=1, dtype=dtype)
+    pos, f = torch.arange(3 * T, device=DEV).view(T, 3).float(), nv.rope_inv_freq(dims)
+    want = nv.nvfp4_rope_axes(x, pos, dims, f)
+    big = torch.zeros(2 * odd, dtype=dtype, device=DEV)
+    strides = (odd if T == 1 else D * H, odd if H == 1 else D, 1)
+    view = big.as_strided((T, H, D), strides)
+    view.copy_(x)
+    assert torch.equal(nv.nvfp4_rope_axes(view, pos, dims, f), want)
+    assert nv.nvfp4_rope_axes(view, pos, dims, f, out=view) is view and torch.equal(view, want)
