@@ -386,7 +386,9 @@ nvfp4_status_t nvfp4_mx8_quantize(const void *x, nvfp4_dtype_t x_dtype, int64_t 
  *                  Of codes and y at least one is needed.
  *   inv_rms        NULL, or fp32 [M] (the backward pass reads it).
  *   M == 0 is valid and touches nothing.
- * A row with a non-finite value makes that row's outputs non-finite (its blocks' scales 255).
+ * A row whose s has an infinity or a NaN gets NaN in inv_rms, in all of y and in all its codes, under
+ * scales of 255; h is the sum as it is.  Other rows are not touched by it (in the backward pass it reaches
+ * dweight).  A finite row has a finite norm also where the sum of its squares is past fp32.
  *
  * Backward, for the gradient dy of y (the straight-through estimator passes it through the
  * quantization) and dh of h (NULL: none): with n = h inv_rms, g = dy weight,

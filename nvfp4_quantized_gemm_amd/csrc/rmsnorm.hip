@@ -4,7 +4,9 @@
 //   inv_rms = 1 / sqrt(mean_k s^2 + eps)           y = s inv_rms weight
 //   codes, scales = MXFP8(y)                       (mx8.hpp)
 // The norm is of the fp32 sum, not of the rounded h: h is rounded once, for the next layer, and y
-// once, to its 8 bits.  Sums of squares and everything before the encoding are fp32.
+// once, to its 8 bits.  Sums of squares and everything before the encoding are fp32; a row whose sum of
+// squares leaves fp32 is summed again times 2^-80 (overflowing_rms).  A row with a non-finite value has no norm:
+// inv_rms, y, codes and scales are NaN.
 //
 // Bound by memory.  One pass: the row stays in registers between the sum of squares and the output, so x and
 // residual are read and h and the codes written once (7.03 B per bf16 element): 16384 x 8192 in 158 to 164 us,
@@ -13,6 +15,9 @@
 //
 // Backward, with n = h inv_rms, g = dy weight, c = mean_k(g n):
 //   dx = inv_rms (g - n c) + dh  (x's gradient and the residual's)      dweight = sum_m dy n
+#include <cfloat>
+#include <cmath>
+
 #include "launch.hpp"
 #include "mx8.hpp"
 
@@ -33,11 +38,11 @@ __device__ __forceinline__ float wave_sum(float v) {
 // and no other wave is waited for.  Otherwise the row is the whole workgroup's, and `red` holds two
 // sets of partials used in turn, so one barrier per row is enough.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float *red, int phase) {
+__device__ __forceinline__ float row_sum(float v, float *red, int set) {
   v = wave_sum(v);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
-    float *r = red + (phase & 1) * W;
+    float *r = red + set * W;
     if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.0f;
@@ -63,6 +68,24 @@ __device__ __forceinline__ void load_weight(const void *w, int w_dtype, int64_t 
   }
 }
 
+// inv_rms of a row s whose mean square + eps is past fp32: both times 2^-160, where no finite row overflows
+// (2^96 a square) and what underflows is below 2^-100 of the sum.  NaN where a value is not finite.  A third set
+// of partials: the rows before and after this one use the other two.
+template <int TPR, int NV>
+__device__ __forceinline__ float overflowing_rms(const float (&s)[NV][8], float *red, const NormArgs &a) {
+  constexpr float kDown = 0x1p-80f;
+  float sq = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = s[j][i] * kDown;
+      sq = fmaf(v, v, sq);
+    }
+  const float square = row_sum<TPR>(sq, red, 2) * a.inv_k + a.eps * kDown * kDown;
+  return square <= FLT_MAX ? kDown / sqrtf(square) : NAN;
+}
+
 }  // namespace
 
 // TPR threads (64, 256 or 1024) hold a row in registers, NV vectors of 8 elements each; workgroups
@@ -72,7 +95,7 @@ template <int DT, int TPR, int NV, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
   constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
   constexpr bool kAhead = TPR < 1024 || NV <= 2;  // 16 waves leave 128 registers: none to look ahead
-  __shared__ float red[TPR > 64 ? 2 * TPR / 64 : 1];
+  __shared__ float red[TPR > 64 ? 3 * TPR / 64 : 1];  // two sets in turn, and one of overflowing_rms
   const int t = threadIdx.x % TPR;
   const int nseg = (int)(a.K / 8);
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -121,8 +144,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
       }
     }
     if (kAhead && m + step < a.M) fetch(m + step);
-    const float mean = row_sum<TPR>(sq, red, phase) * a.inv_k;
-    const float inv_rms = 1.0f / sqrtf(mean + a.eps);
+    const float square = row_sum<TPR>(sq, red, phase & 1) * a.inv_k + a.eps;
+    // the same for all of a row's threads, so they go together to the barrier inside
+    const float inv_rms = square <= FLT_MAX ? 1.0f / sqrtf(square) : overflowing_rms<TPR, NV>(s, red, a);
     if (a.inv_rms && t == 0) a.inv_rms[m] = inv_rms;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -223,7 +247,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_backward(Norm
       }
     }
     if (kAhead && m + step < a.M) fetch(m + step);
-    const float c = row_sum<TPR>(dot, red, phase) * a.inv_k;
+    const float c = row_sum<TPR>(dot, red, phase & 1) * a.inv_k;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int seg = j * TPR + t;
