@@ -379,7 +379,8 @@ nvfp4_status_t nvfp4_mx8_quantize(const void *x, nvfp4_dtype_t x_dtype, int64_t 
  *   K              32 .. 32768, K % 32 == 0.
  *   weight         NULL, or [K] of weight_dtype (fp32 or bf16), 16-byte aligned.
  *   eps            finite, > 0 (else NVFP4_ERR_MODE).
- *   h              NULL, or [M][ld_h] of dtype.  May be x or residual itself (same pitch).
+ *   h              NULL, or [M][ld_h] of dtype.  h, or y of the same dtype, may be x or residual itself (same
+ *                  pitch, else NVFP4_ERR_STRIDE); otherwise no written array may overlap another array.
  *   codes, scales  both or neither; codes 16-byte aligned.
  *   y              NULL, or [M][ld_y] of y_dtype.  fake_quantize != 0: y receives the values that
  *                  the MXFP8 codes stand for (quantization-aware training), else the norm itself.
@@ -394,7 +395,8 @@ nvfp4_status_t nvfp4_mx8_quantize(const void *x, nvfp4_dtype_t x_dtype, int64_t 
  * quantization) and dh of h (NULL: none): with n = h inv_rms, g = dy weight,
  *     dx = inv_rms (g - n mean_k(g n)) + dh   (the gradient of x and, the same, of residual)
  *     dweight[k] = sum_m dy n                 fp32
- *   dy, h, dh, dx  of dtype at their own pitches; dx may be dy or dh itself (same pitch).
+ *   dy, h, dh, dx  of dtype at their own pitches; dx may be dy, h or dh itself (same pitch, else
+ *                  NVFP4_ERR_STRIDE) and must not overlap them otherwise.
  *   dweight        NULL, or [K] fp32, 16-byte aligned; then workspace holds at least
  *                  nvfp4_rmsnorm_backward_workspace_bytes(M, K) bytes, 16-byte aligned, with no
  *                  initialization.  Sums run in a fixed order: equal inputs give equal bits.

@@ -126,6 +126,12 @@ inline nvfp4_status_t check_pitch(int64_t ld, int64_t M, int64_t K) {
 inline bool rows_aligned(const void *p, int64_t ld, nvfp4_dtype_t t) {
   return !p || (aligned(p, 16) && (ld * elem_size(t)) % 16 == 0);
 }
+// A written [M][ld] array at an input's own address must have its rows (or be one row of the same elements): rows
+// are read while others are written.
+inline bool in_place_fits(const void *out, int64_t ld_out, nvfp4_dtype_t t_out, const void *in, int64_t ld_in,
+                          nvfp4_dtype_t t_in, int64_t M) {
+  return !out || out != in || (t_out == t_in && (M <= 1 || ld_out == ld_in));
+}
 // [T][H][D] rows at a token and a head pitch: offsets of 64 bits, and, where they are written, rows
 // that do not overlap (tokens outermost or heads outermost)
 inline bool head_rows_fit(int64_t T, int64_t H, int64_t D, int64_t ld_t, int64_t ld_h, bool written) {

@@ -44,6 +44,10 @@ nvfp4_status_t nvfp4_rmsnorm(const void *x, int64_t ld_x, const void *residual, 
   if (!rows_aligned(x, ld_x, dtype) || !rows_aligned(residual, ld_residual, dtype) || !rows_aligned(h, ld_h, dtype) ||
       !rows_aligned(y, ld_y, y_dtype) || !aligned(weight, 16) || !aligned(codes, 16) || !aligned(inv_rms, 4))
     return NVFP4_ERR_ALIGN;
+  if (!in_place_fits(h, ld_h, dtype, x, ld_x, dtype, M) || !in_place_fits(h, ld_h, dtype, residual, ld_residual, dtype, M) ||
+      !in_place_fits(y, ld_y, y_dtype, x, ld_x, dtype, M) ||
+      !in_place_fits(y, ld_y, y_dtype, residual, ld_residual, dtype, M))
+    return NVFP4_ERR_STRIDE;
   if ((st = check_device()) != NVFP4_OK) return st;
   st = debug_scan(stream, {finite_values(x, dtype, M, K, ld_x), finite_values(residual, dtype, M, K, ld_residual),
                            finite_values(weight, weight_dtype, 1, K, K)});
@@ -75,6 +79,9 @@ nvfp4_status_t nvfp4_rmsnorm_backward(const void *dy, int64_t ld_dy, const void 
     if (!rows_aligned(dy, ld_dy, dtype) || !rows_aligned(h, ld_h, dtype) || !rows_aligned(dh, ld_dh, dtype) ||
         !rows_aligned(dx, ld_dx, dtype) || !aligned(weight, 16) || !aligned(inv_rms, 4))
       return NVFP4_ERR_ALIGN;
+    if (!in_place_fits(dx, ld_dx, dtype, dy, ld_dy, dtype, M) || !in_place_fits(dx, ld_dx, dtype, h, ld_h, dtype, M) ||
+        !in_place_fits(dx, ld_dx, dtype, dh, ld_dh, dtype, M))
+      return NVFP4_ERR_STRIDE;
   }
   if (dweight) {
     if (M > 0 && (!workspace || workspace_bytes < nvfp4_rmsnorm_backward_workspace_bytes(M, K)))

@@ -68,6 +68,18 @@ def test_rmsnorm_weight(dtype, form):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M,K", [(3, 96), (3000, 96), (300, 4608), (5, 32768)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_gradients_in_an_input_s_place(M, K, dtype):
+    dy, h, dh = (rnd(M, K, seed=i, dtype=dtype) for i in range(3))
+    inv, w = 1 / h.float().square().mean(1).sqrt(), 1 + 0.1 * rnd(K, seed=5)
+    dx, dw = nv.nvfp4_rmsnorm_backward(dy, h, inv, w, dh)
+    for i in range(3):
+        t = [dy.clone(), h.clone(), dh.clone()]
+        got, gw = nv.nvfp4_rmsnorm_backward(t[0], t[1], inv, w, t[2], dx=t[i])
+        assert got is t[i] and torch.equal(got, dx) and torch.equal(gw, dw), i
+
+
 HEADS = {"dense": lambda t: t, "expanded heads": lambda t: t[:, :1].expand(t.shape), "off 16 bytes": off16,
          "expanded tokens": lambda t: t[:1].expand(t.shape), "heads first": lambda t: t.transpose(0, 1).contiguous().transpose(0, 1),
          "strided": lambda t: t.repeat_interleave(2, 2)[..., ::2],
