@@ -478,6 +478,14 @@ def _launch_device(ref: torch.Tensor) -> int:
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
+def _written(t: torch.Tensor, name: str):
+    """Mark a caller's tensor as written, for autograd, which cannot see stores through an address; refuse one whose
+    gradient is being recorded, as the call records none (torch's own out= does the same)."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} is written in place and requires a gradient, which this call does not record")
+    torch._C._increment_version((t,))
+
+
 def _dense(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
     """Address of a dense tensor of the given shape (a tuple), type and device."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
@@ -520,10 +528,12 @@ def nvfp4_mx8_quantize(x: torch.Tensor, *, codes=None, scales=None, stream=None)
         codes = torch.empty(M, K, dtype=_u8, device=x.device)
     else:
         _dense(codes, "codes", (M, K), _u8, dev)
+        _written(codes, "codes")
     if scales is None:
         scales = torch.empty(M, K // 32, dtype=_u8, device=x.device)
     else:
         _dense(scales, "scales", (M, K // 32), _u8, dev)
+        _written(scales, "scales")
     st = lib().nvfp4_mx8_quantize(x.data_ptr(), _dtype_code(x.dtype), M, K, ld, codes.data_ptr(), scales.data_ptr(),
                                   _current_stream(dev))
     if st:
@@ -568,6 +578,7 @@ def nvfp4_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight:
             ld_h, p_h = K, h.data_ptr()
     if h is not None and not p_h:
         ld_h, p_h = _pitch(h, "h", shape, dtype, dev), h.data_ptr()
+        _written(h, "h")
     if weight is not None:
         p_w, w_code = _weight(weight, K, dev)
     if mx8:
@@ -618,6 +629,7 @@ def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, inv_rms: torch.Ten
         dx, ld_dx = torch.empty(M, K, dtype=dtype, device=device), K
     else:
         ld_dx = _pitch(dx, "dx", shape, dtype, dev)
+        _written(dx, "dx")
     L = lib()
     dw = None
     if dweight:
@@ -707,6 +719,7 @@ def nvfp4_mx_gemm_w4a8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
         out, ldc = torch.empty(M, N, dtype=out_dtype, device=a.device), N
     else:
         ldc = _pitch(out, "out", (M, N), out.dtype, dev)
+        _written(out, "out")
     st = lib().nvfp4_mx_gemm_w4a8(a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, N, K,
                                   out.data_ptr(), _dtype_code(out.dtype), ldc, _current_stream(dev))
     if st:
@@ -744,6 +757,7 @@ def nvfp4_rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_fre
         raise ValueError("out must have x's shape, type and device")
     else:
         yt, yh, yd = out.stride()
+        _written(out, "out")
     if xd != 1 or yd != 1:
         raise ValueError("x and out must have unit stride along D")
     if T == 1:  # the pitch of a single token or head is never used, whatever it is
