@@ -2,6 +2,7 @@
 //
 // Y[m][n] = sum_k a[m][k] Xa[m][k / 32] b[n][k] Xb[n][k / 32]: E4M3 codes times E2M1 codes under
 // E8M0 scales, exact products, fp32 sums.
+#include <cmath>
 #include <type_traits>
 
 #include "epilogue.hpp"
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(256) void k_w4a8_generic(const uint8_t *__restrict_
     const int64_t m = t / N, n = t % N;
     float acc = 0.0f;
     for (int64_t k = 0; k < K; k += kMx8Blk) {
-      const float X = mx8_scale_value(as[(m * K + k) / kMx8Blk]) * mx8_scale_value(bs[(n * K + k) / kMx8Blk]);
+      const int ea = as[(m * K + k) / kMx8Blk], eb = bs[(n * K + k) / kMx8Blk];
       float part = 0.0f;
       for (int i = 0; i < kMx8Blk; i += 2) {
         const uint32_t w = b[(n * K + k + i) / 2];
@@ -61,7 +62,8 @@ __global__ __launch_bounds__(256) void k_w4a8_generic(const uint8_t *__restrict_
         part = fmaf(e4m3_to_f32(a[m * K + k + i]), q.x, part);
         part = fmaf(e4m3_to_f32(a[m * K + k + i + 1]), q.y, part);
       }
-      acc = fmaf(part, X, acc);
+      // both scales in one exponent: their product alone may leave fp32 where the scaled sum does not
+      acc += ea == 255 || eb == 255 ? NAN : ldexpf(part, ea + eb - 254);
     }
     if (OUT == 0) static_cast<float *>(c)[m * ldc + n] = acc;
     else static_cast<__bf16 *>(c)[m * ldc + n] = (__bf16)acc;

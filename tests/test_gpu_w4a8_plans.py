@@ -94,3 +94,40 @@ def test_product(M, N, K, dtype):
     assert worst(y, *values(*ops)) <= 1
     assert (big[:M, N:] == 7).all() and (big[M] == 7).all()
     assert torch.equal(nv.nvfp4_mx_gemm_w4a8(*ops, dtype), y)  # a dense result, where rows may not be 16-byte aligned
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_many_short_rows_under_any_scales(dtype):
+    """More rows of K = 32 than the few-row kernel's grid takes.  Scales whose product alone leaves fp32, both ways."""
+    M, N, K = GENERIC[0]
+    print("[w4a8 plan]", M, N, K, dtype, plan(M, N, K), flush=True)
+    a, sa, b, sb = operands(M, N, K, seed=1)
+    sa.copy_(torch.tensor([127, 5, 245, 246, 100], dtype=torch.uint8, device=DEV)[torch.arange(M, device=DEV) % 5, None])
+    sb.copy_(torch.tensor([127, 240, 3, 250], dtype=torch.uint8, device=DEV)[torch.arange(N, device=DEV) % 4, None])
+    a[7::11] = 0
+    a[8::11, 1:] = 0  # one small value: 2^-9
+    a[8::11, 0] = 1
+    y = nv.nvfp4_mx_gemm_w4a8(a, sa, b, sb, dtype)
+    A, B = values(a, torch.full_like(sa, 127), b, torch.full_like(sb, 127))
+    X = torch.exp2(sa.double() + sb.double().t() - 254)  # [M, N]
+    Bt = B.t().contiguous()
+    Y, R = (A @ Bt) * X, (A.abs() @ Bt.abs()) * X
+    fits = R < 3.3e38
+    tol = 1e-5 * R + (V * Y.abs() if dtype == BF else 0) + 2.0 ** -133
+    assert ((y.double() - Y).abs() <= tol)[fits].all()
+    over = Y.abs() > 3.5e38
+    assert over.any() and (y.double() == torch.where(Y > 0, torch.inf, -torch.inf))[over].all()
+    assert (y[7::11] == 0).all()
+
+
+@pytest.mark.gpu
+def test_one_row_of_eight_million():
+    M, N, K = GENERIC[1]
+    print("[w4a8 plan]", M, N, K, plan(M, N, K), flush=True)
+    ops = operands(M, N, K, seed=2)
+    y = nv.nvfp4_mx_gemm_w4a8(*ops, F32)
+    A, B = values(*ops)
+    Bt = B.t().contiguous()
+    # one chain of K / 32 fp32 additions of blocks of 32
+    assert ((y.double() - A @ Bt).abs() <= (K / 32 + 32) * 2.0 ** -24 * (A.abs() @ Bt.abs())).all()
