@@ -475,7 +475,8 @@ def _launch_device(ref: torch.Tensor) -> int:
 
 # Raw handle of the current stream of a device (current_stream() without making an object).  The calls below
 # that take a stream run as under ``with torch.cuda.stream(stream)``: what they allocate is that stream's.
-_current_stream = torch._C._cuda_getCurrentRawStream
+# None on a torch without device bindings, where no operand gets as far.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _written(t: torch.Tensor, name: str):
