@@ -416,8 +416,10 @@ nvfp4_status_t nvfp4_rmsnorm_backward(const void *dy, int64_t ld_dy, const void 
 /* ---------------------------------------------------------------------------------------------
  * W4A8 product: Y[M][N] = A B^T with A [M][K] MXFP8 (codes and scales as nvfp4_mx8_quantize and
  * nvfp4_rmsnorm write them) and B [N][K] canonical MXFP4 (nvfp4_mx_quantize), for prompts and for
- * single tokens.  Products are exact and accumulate in fp32; only the summation order differs from
- * dequantize-then-matmul.  a, b 16-byte aligned, a_scales, b_scales 4-byte aligned; c as for
+ * single tokens.  Operands are widened to bf16 with their scales, products are exact and accumulate in
+ * fp32: only the summation order differs from dequantize-then-matmul -- except under activation scale
+ * bytes 0 to 2 (blocks below 2^-116), where operands are rounded to multiples of bf16's least number,
+ * 2^-133: Y may be off by another 2^-133 sum_k |b Xb|.  a, b 16-byte aligned, a_scales, b_scales 4-byte aligned; c as for
  * nvfp4_gemm (fp32 or bf16, base 16-byte aligned, any ldc >= N).  K % 32 == 0; M, N, K < 2^30.
  * M == 0 or N == 0 is valid and touches nothing.
  * ------------------------------------------------------------------------------------------- */

@@ -1,7 +1,7 @@
 // MXFP8 quantize, and the product of MXFP8 activations with MXFP4 weights (W4A8), for gfx950.
 //
 // Y[m][n] = sum_k a[m][k] Xa[m][k / 32] b[n][k] Xb[n][k / 32]: E4M3 codes times E2M1 codes under
-// E8M0 scales, exact products, fp32 sums.
+// E8M0 scales, exact products (of operands from 2^-133 on), fp32 sums.
 #include <cmath>
 #include <type_traits>
 
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256) void k_w4a8_generic(const uint8_t *__restrict_
 // The matrix instruction that takes E4M3 and E2M1 codes with E8M0 scales as they are sums groups of eight
 // products in a window of 13 bits below the group's largest: measured, a product under 2^-13 of it is
 // dropped, and a product over wide-ranging values came out 3e-5 of sum |a b| off.  That is no fp32 sum, so
-// the codes are widened to bf16 with their scale (exact: at most 4 significant bits; one conversion
+// the codes are widened to bf16 with their scale (exact down to 2^-133: at most 4 significant bits; one conversion
 // instruction per two values) and multiplied by v_mfma_f32_32x32x16_bf16, at half the rate.
 //
 // Operands of a 64-k step: lane (r, h) = (l % 32, l / 32) takes block h of row r: 32 activation bytes, 16
@@ -118,7 +118,8 @@ __device__ __forceinline__ uint32_t scale_turn(int i) { return (8 * i + 9) & 31;
 __device__ __forceinline__ float scale_at(uint32_t word, uint32_t turn) {
   return __uint_as_float(__builtin_amdgcn_alignbit(word, word, turn));
 }
-// 8 E4M3 codes of words lo, hi, or the 8 E2M1 codes of a word, times their scale: exact in bf16.
+// 8 E4M3 codes of words lo, hi, or the 8 E2M1 codes of a word, times their scale: exact in bf16, but for E4M3
+// under scale bytes 0 to 2, whose steps of 2^-136 to 2^-134 are below bf16's least number, 2^-133.
 __device__ __forceinline__ bf16x8 widen_act(uint32_t lo, uint32_t hi, float X) {
   const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, X, false);
   const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, X, true);

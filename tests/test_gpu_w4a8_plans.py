@@ -131,3 +131,17 @@ def test_one_row_of_eight_million():
     Bt = B.t().contiguous()
     # one chain of K / 32 fp32 additions of blocks of 32
     assert ((y.double() - A @ Bt).abs() <= (K / 32 + 32) * 2.0 ** -24 * (A.abs() @ Bt.abs())).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 24, 150, 600])
+@pytest.mark.parametrize("K", [96, 160, 1152])
+@pytest.mark.parametrize("sa", [0, 1, 2, 3])
+@pytest.mark.parametrize("sb", [127, 235, 250])
+def test_smallest_activation_scales(M, K, sa, sb):
+    N = 70
+    ops = operands(M, N, K, seed=3, sa=(sa, sa + 1), sb=(sb, sb + 1))
+    A, B = values(*ops)
+    # a product of numbers below 2^-126 may itself be lost under fp32's least subnormal
+    more = (2.0 ** -133 if sa < 3 else 0) * B.abs().sum(1) + K * 2.0 ** -149
+    assert worst(nv.nvfp4_mx_gemm_w4a8(*ops, F32), A, B, more) <= 1
