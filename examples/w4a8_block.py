@@ -3,8 +3,9 @@
   serving   residual + RMS norm -> MXFP8 -> QKV product with an MXFP4 weight -> rotary positions of time, height and
             width on q and k, in place in the QKV output -> attention (torch, fp32) -> MXFP8 -> output projection ->
             the next norm with the residual's addition
-  training  the same block with bf16 weights in quantization-aware training: the norm's output fake-quantized to
-            MXFP8, the weights to NVFP4, straight-through gradients, a few steps of gradient descent
+  training  the same block with bf16 weights in quantization-aware training: what serving rounds is rounded to the
+            same values (MXFP8 inputs of both products, MXFP4 weights), straight-through gradients, a few steps of
+            gradient descent
 
   python examples/w4a8_block.py [--grid 4,32,32] [--heads 16] [--head-dim 72] [--steps 3]
 """
@@ -54,14 +55,40 @@ class ServingBlock:
         return after.codes, after.scales, after.h
 
 
+class StraightThrough(torch.autograd.Function):
+    """Takes the quantized values of x forward and their gradient back to x."""
+
+    @staticmethod
+    def forward(ctx, x, quantized):
+        ctx.dtype = x.dtype
+        return quantized.view_as(quantized)
+
+    @staticmethod
+    def backward(ctx, grad):
+        return grad.to(ctx.dtype), None
+
+
+def mx4_weight(w):
+    """The values of w's MXFP4 codes (exact in bf16)."""
+    return StraightThrough.apply(w, nv.nvfp4_mx_dequantize(*nv.nvfp4_mx_quantize(w.detach()), w.dtype))
+
+
+def mx8_activation(t, dtype):
+    """The values of t's MXFP8 codes (exact in bf16)."""
+    codes, scales = nv.nvfp4_mx8_quantize(t.detach())
+    blocks = codes.view(torch.float8_e4m3fn).float().view(*scales.shape, 32)
+    values = blocks * scales.view(torch.float8_e8m0fnu).float().unsqueeze(-1)
+    return StraightThrough.apply(t, values.view(t.shape).to(dtype))
+
+
 def training_block(x, residual, positions, axis_dims, inv_freq, heads, w_qkv, w_out, norm_weight):
     """The block for quantization-aware training: (output, residual stream), differentiable."""
     T, hidden = x.shape
     y, h = nv.rmsnorm(x, residual, norm_weight, fake_quantize=True)
-    qkv = F.linear(y, nv.fake_quantize_ste(w_qkv)).view(T, 3 * heads, hidden // heads)
+    qkv = F.linear(y, mx4_weight(w_qkv)).view(T, 3 * heads, hidden // heads)
     q, k, v = qkv.split(heads, 1)
     q, k = (nv.rope_axes(t, positions, axis_dims, inv_freq) for t in (q, k))
-    return F.linear(attention(q, k, v).to(x.dtype), nv.fake_quantize_ste(w_out)), h
+    return F.linear(mx8_activation(attention(q, k, v), x.dtype), mx4_weight(w_out)), h
 
 
 def make_inputs(tokens: int, hidden: int, device="cuda", seed: int = 0):
