@@ -526,7 +526,8 @@ __global__ __launch_bounds__(Cfg::kThreads) __attribute__((amdgpu_waves_per_eu(C
 // ---- few rows -----------------------------------------------------------------------------------------
 //
 // Bound by latency: the weight is read once, 17/32 B a value, and there are few bytes to a CU (4608 x 1152
-// for one row: 3.2 us, 2.0 of them the launch and 2.06 a bare read of the weight; 4096 x 4096: 4.9 us).
+// for one row: 3.2 us, 2.0 of them the launch and 2.06 a bare read of the weight; 4096 x 4096: 4.9 us; the
+// weight in the last-level cache).
 // A workgroup owns 16 NT output columns and up to 16 MT rows; its W waves take every W-th run of U 128-k
 // chunks and their sums are added in LDS in the order of the runs.  Operands straight from memory: lane (r, q) = (l % 16, l / 16)
 // takes block q of row r, and its 32 values make four v_mfma_f32_16x16x32_bf16 of 8 k from every block.
@@ -744,7 +745,9 @@ hipError_t launch_rows(const W4A8Args &g, hipStream_t s) {
 // M = 64: 32 x 32 8.0 us and 64 x 32 10.0 (1152 x 4608), 21.3 and 16.5 (8192 x 8192, where 32 x 32 needs two
 // rounds); M = 512 x 4608 x 1152: 128 x 64 12.2, 128 x 128 11.1; M = 2048 x 8192 x 8192: 128 x 128 209,
 // 256 x 256 192.  Past one round the 128 x 128 tiles, two of which share a CU, and the 256 x 256 tiles are
-// compared by what their rounds cost.
+// compared by what their rounds cost.  All of this was measured on weights of 1152 to 8192 columns that stay in the
+// last-level cache.  Few rows of wider weights also take the tall tiles, most of whose rows are copies: N = 12288,
+// K = 3072 10.2 us for one row and 28672 x 8192 51.1, where a read of the weight takes 3.4 and 21.2.
 template <int OUT>
 hipError_t launch_out(const W4A8Args &g, hipStream_t s) {
   auto tiles = [&](int64_t r, int64_t c) { return ((g.M + r - 1) / r) * ((g.N + c - 1) / c); };
