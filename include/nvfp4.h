@@ -50,7 +50,7 @@ typedef enum {
   NVFP4_OK = 0,
   NVFP4_ERR_NULL = 1,      /* a required pointer is NULL */
   NVFP4_ERR_SHAPE = 2,     /* M < 0, N < 0, K < 16, K % 16 != 0, a bad block size, or a size overflow */
-  NVFP4_ERR_STRIDE = 3,    /* a leading dimension is smaller than the row it must hold */
+  NVFP4_ERR_STRIDE = 3,    /* a leading dimension is smaller than the row it must hold, or differs in place */
   NVFP4_ERR_ALIGN = 4,     /* a pointer or row pitch breaks the stated alignment */
   NVFP4_ERR_DTYPE = 5,     /* unknown dtype, or a dtype the call does not accept */
   NVFP4_ERR_MODE = 6,      /* unknown mode */

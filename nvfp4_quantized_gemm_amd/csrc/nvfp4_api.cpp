@@ -14,7 +14,7 @@ const char *nvfp4_status_string(nvfp4_status_t s) {
     case NVFP4_OK: return "ok";
     case NVFP4_ERR_NULL: return "a required pointer is NULL";
     case NVFP4_ERR_SHAPE: return "invalid shape (M, N >= 1; K >= 16 and K % 16 == 0)";
-    case NVFP4_ERR_STRIDE: return "leading dimension too small";
+    case NVFP4_ERR_STRIDE: return "leading dimension too small, or not the input's in place";
     case NVFP4_ERR_ALIGN: return "pointer or row pitch misaligned";
     case NVFP4_ERR_DTYPE: return "unsupported dtype";
     case NVFP4_ERR_MODE: return "unknown mode";
