@@ -484,7 +484,7 @@ def _written(t: torch.Tensor, name: str):
     gradient is being recorded, as the call records none (torch's own out= does the same)."""
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} is written in place and requires a gradient, which this call does not record")
-    torch._C._increment_version((t,))
+    torch.autograd.graph.increment_version(t)
 
 
 def _dense(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
