@@ -457,6 +457,37 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
                                const float *inv_freq, nvfp4_rope_layout_t layout, int inverse, void *y,
                                int64_t ldy_token, int64_t ldy_head, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Softmax attention of whole prompts and images:
+ *     o_i = sum_j p_ij v_j,   p_ij = exp(scale q_i . k_j - lse_i),   lse_i = log sum_j exp(scale q_i . k_j)
+ * over the keys j of query i's sequence, with causal != 0 only those with j <= i + n_k - n_q (positions
+ * inside the sequence, which has n_q queries and n_k keys: the last query attends all keys).  A query that
+ * attends no key gets o = 0 and lse = -infinity.
+ *
+ *   q, out       bf16 [Tq][Hq][D] at token pitch ld*_token and head pitch ld*_head (elements, whole 16
+ *                bytes, 16-byte aligned): the queries inside a QKV linear's output are one such tensor.
+ *   k, v         bf16 [Tk][Hkv][D], the same; Hq a multiple of Hkv, query head h reads key head
+ *                h / (Hq / Hkv).
+ *   D            8 .. 128, D % 8 == 0.   Token pitches < 2^23; Hq (max(Tq, Tk) / 32 + B + 1) < 2^23,
+                Hq <= 2^16, B <= 2^20.
+ *   cu_q, cu_k   both NULL: B sequences of Tq / B queries and Tk / B keys (whole numbers).  Else device
+ *                int32 [B + 1] (they may be one array): sequence b has the rows cu[b] .. cu[b + 1] - 1, in
+ *                order, of any lengths (0 too).  Rows past the last sequence are not read, and of out and
+ *                lse left as they were.  Offsets are taken into [0, T], so no content makes a call read or
+ *                write outside its arrays.
+ *   scale        finite, > 0 (else NVFP4_ERR_MODE).
+ *   out          may be q itself (same pitches), and otherwise must not overlap an input.
+ *   lse          NULL, or fp32 [Hq][Tq] (the backward pass reads it).
+ * Scores, exponentials and sums are fp32; the exponentials are rounded to bf16 for their product with v.
+ * Infinities and NaN reach only the queries that attend them.  Tq == 0, Hq == 0 or B == 0 is valid and
+ * touches nothing; Tk == 0 writes zeros.
+ * ------------------------------------------------------------------------------------------- */
+nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_head, const void *k, int64_t ldk_token,
+                               int64_t ldk_head, const void *v, int64_t ldv_token, int64_t ldv_head, int64_t Tq,
+                               int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, const int32_t *cu_q,
+                               const int32_t *cu_k, int64_t B, int causal, float scale, void *out, int64_t ldo_token,
+                               int64_t ldo_head, float *lse, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

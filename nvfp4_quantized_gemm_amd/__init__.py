@@ -8,6 +8,7 @@ kernels of ``libnvfp4.so``; there is no fallback.  The function names mirror the
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from enum import IntEnum
 from typing import NamedTuple
@@ -50,6 +51,7 @@ EXPORTED = (
     "nvfp4_quantize_noalloc", "nvfp4_set_debug_checks",
     "nvfp4_mx8_quantize", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes", "nvfp4_rmsnorm_backward",
     "nvfp4_mx_gemm_w4a8", "nvfp4_rope_axes",
+    "nvfp4_attention",
 )
 
 _lib = None
@@ -142,6 +144,9 @@ def lib():
     L.nvfp4_rope_axes.restype = _i
     L.nvfp4_rope_axes.argtypes = [_vp, _i, _i64, _i64, _i64, _i64, _i64, _vp, _i, _vp, _vp, _i, _i, _vp, _i64, _i64,
                                   _vp]
+    heads = [_vp, _i64, _i64]  # address, token pitch, head pitch
+    L.nvfp4_attention.restype = _i
+    L.nvfp4_attention.argtypes = heads * 3 + [_i64] * 5 + [_vp, _vp, _i64, _i, ctypes.c_float] + heads + [_vp, _vp]
     _lib = L
     return L
 
@@ -456,7 +461,7 @@ def nvfp4_mx_gemm(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sc
 ROPE_PAIRS, ROPE_HALVES = 0, 1
 
 
-_u8, _f32 = torch.uint8, torch.float32
+_u8, _f32, _bf16, _i32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
 
 
 # The checks below run on every call, also where the call is one token's and takes as long as its launch, so
@@ -803,6 +808,76 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, axis_dims, inv_freq: tor
     return _RopeAxes.apply(x, positions, tuple(axis_dims), inv_freq, layout)
 
 
+# ---- attention ----------------------------------------------------------------------------------
+
+def _heads(t: torch.Tensor, name: str, shape, dev: int):
+    """(address, token pitch, head pitch) of a bf16 tensor [T, H, D] with unit stride along D.  The pitch of a single
+    token or head is never used, whatever it is."""
+    if t.shape != shape or t.dtype is not _bf16 or t.get_device() != dev:
+        raise ValueError(f"{name} must be {_bf16} {tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    st, sh, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride along D")
+    return t.data_ptr(), st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
+
+
+def _offsets(cu_q, cu_k, batch: int, dev: int):
+    """(address of cu_q, of cu_k, sequences)."""
+    if cu_q is None and cu_k is None:
+        return 0, 0, batch
+    if cu_q is None or cu_k is None:
+        raise ValueError("cu_q and cu_k are given together")
+    n = cu_q.shape
+    if len(n) != 1 or n[0] < 1:
+        raise ValueError("cu_q must hold the sequences' offsets, one more than sequences")
+    return _dense(cu_q, "cu_q", n, _i32, dev), _dense(cu_k, "cu_k", n, _i32, dev), n[0] - 1
+
+
+def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False, scale: float | None = None,
+                    cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, batch: int = 1,
+                    save_lse: bool = False, out=None, lse=None, stream=None):
+    """Softmax attention of q [Tq, Hq, D] over k, v [Tk, Hkv, D] (bf16, token and head strides free: views of a QKV
+    output are read in place).  Hq is a multiple of Hkv.  Returns (out, lse): out bf16 [Tq, Hq, D], lse fp32 [Hq, Tq], the
+    log sums of exponentials that the backward pass reads (None without save_lse or a given lse).
+
+    cu_q, cu_k: int32 offsets [sequences + 1] of packed sequences; without them the rows are `batch` sequences of equal
+    length.  causal: query i of n_q attends keys up to i + n_k - n_q.  scale: D ** -0.5 by default.  Queries without keys
+    get 0 and -inf; so do, in new tensors, rows past the last sequence, which in given ones are left as they were."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_attention(q, k, v, causal=causal, scale=scale, cu_q=cu_q, cu_k=cu_k, batch=batch,
+                                   save_lse=save_lse, out=out, lse=lse)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [T, H, D]")
+    Tq, Hq, D = shape = q.shape
+    Tk, Hkv, _ = k.shape
+    dev = _launch_device(q)
+    p_q, qt, qh = _heads(q, "q", shape, dev)
+    p_k, kt, kh = _heads(k, "k", (Tk, Hkv, D), dev)
+    p_v, vt, vh = _heads(v, "v", (Tk, Hkv, D), dev)
+    p_cq, p_ck, batch = _offsets(cu_q, cu_k, batch, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=_bf16, device=q.device) if p_cq == 0 else torch.zeros(shape, dtype=_bf16, device=q.device)
+        p_o, ot, oh = out.data_ptr(), Hq * D, D
+    else:
+        p_o, ot, oh = _heads(out, "out", shape, dev)
+        _written(out, "out")
+    p_l = 0
+    if lse is not None:
+        p_l = _dense(lse, "lse", (Hq, Tq), _f32, dev)
+        _written(lse, "lse")
+    elif save_lse:
+        lse = torch.empty(Hq, Tq, dtype=_f32, device=q.device) if p_cq == 0 else \
+            torch.full((Hq, Tq), -math.inf, dtype=_f32, device=q.device)
+        p_l = lse.data_ptr()
+    st = lib().nvfp4_attention(p_q, qt, qh, p_k, kt, kh, p_v, vt, vh, Tq, Tk, Hq, Hkv, D, p_cq, p_ck, batch,
+                               1 if causal else 0, D ** -0.5 if scale is None else scale, p_o, ot, oh, p_l,
+                               _current_stream(dev))
+    if st:
+        raise NVFP4Error(st, "nvfp4_attention")
+    return out, lse
+
+
 __all__ = [
     "Status", "NVFP4Error", "lib", "LIB_PATH", "EXPORTED", "F32", "BF16", "W4A4", "W4A16",
     "SCALE_DYNAMIC", "SCALE_STATIC", "nvfp4_set_debug_checks",
@@ -816,4 +891,5 @@ __all__ = [
     "nvfp4_mx8_quantize", "RMSNormOutput", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes",
     "nvfp4_rmsnorm_backward", "rmsnorm", "nvfp4_mx_gemm_w4a8",
     "ROPE_PAIRS", "ROPE_HALVES", "rope_inv_freq", "nvfp4_rope_axes", "rope_axes",
+    "nvfp4_attention",
 ]

@@ -1,0 +1,187 @@
+// Softmax attention of whole prompts and images (gfx950):
+//   O[i] = sum_j softmax_j(scale q_i k_j) v_j,   lse[i] = log sum_j exp(scale q_i k_j)
+// over packed sequences, with query heads that share key heads, causal (aligned at the ends) or not.
+//
+// A wave has 32 queries as the columns of its products, so that a query's softmax is a lane's (and its
+// partner's in the other half): S^T = K Q^T gives a lane 16 of 32 keys of its query, the exponentials are
+// rounded to bf16 where they are and multiply as they lie, O^T += V^T P^T, and the running maximum and sum
+// are one register each.  Keys and values pass through LDS in tiles of 64, two in turn; V^T is read from
+// its rows by the transposing LDS read.
+#include "attention.hpp"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kKeys = 64;  // keys per tile
+
+// KS: 16-value steps of a head in S; DB: 32-value blocks in O; NW waves of 32 queries.
+template <int KS, int DB, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attention(const AttentionArgs a) {
+  constexpr int P = 4 * DB, BQ = 32 * NW;
+  constexpr int kTile = kKeys * P * 16;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // Which block of which head: neighbouring workgroups lie on different XCDs, so where the heads divide
+  // evenly each XCD takes its own, and all blocks that read a key head's rows share an L2.  Causal blocks
+  // with many keys first.
+  int head, slot;
+  {
+    const int items = a.slots * a.Hq, w = blockIdx.x;
+    const int per = a.Hq % 8 == 0 ? a.Hq / 8 : a.Hq, i = a.Hq % 8 == 0 ? w >> 3 : w, x = a.Hq % 8 == 0 ? (w & 7) * per : 0;
+    (void)items;
+    if (a.causal) {
+      slot = a.slots - 1 - i / per;
+      head = x + i % per;
+    } else {
+      head = x + i / a.slots;
+      slot = i % a.slots;
+    }
+  }
+  int b, blk;
+  find_block<BQ>(slot, a.cu_q, a.B, a.Tq, a.per_q, lane, b, blk);
+  const SeqRows sq = seq_rows(a.cu_q, b, a.Tq, a.per_q), sk = seq_rows(a.cu_k, b, a.Tk, a.per_k);
+  if (blk < 0 || blk * BQ >= sq.n) return;
+  const int kv = head / a.group, q0 = blk * BQ + 32 * wave, query = q0 + c, ahead = sk.n - sq.n;
+
+  const uint16_t *q = static_cast<const uint16_t *>(a.q) + sq.begin * a.ldq_t + head * a.ldq_h;
+  const uint16_t *k = static_cast<const uint16_t *>(a.k) + sk.begin * a.ldk_t + kv * a.ldk_h;
+  const uint16_t *v = static_cast<const uint16_t *>(a.v) + sk.begin * a.ldv_t + kv * a.ldv_h;
+  bf16x8 Q[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) Q[s] = load_column_operand(q, a.ldq_t, query, sq.n, s, a.D, lane);
+
+  // keys 0 .. limit of this lane's query; the workgroup's tiles, and this wave's
+  const int limit = a.causal ? min(query + ahead, sk.n - 1) : sk.n - 1;
+  const int last_wg = a.causal ? min(min((blk + 1) * BQ, sq.n) - 1 + ahead, sk.n - 1) : sk.n - 1;
+  const int last_wave = a.causal ? min(q0 + 31 + ahead, sk.n - 1) : sk.n - 1;
+  const int first_limit = a.causal ? min(q0 + ahead, sk.n - 1) : sk.n - 1;
+  const int tiles = q0 - 32 * wave < sq.n && last_wg >= 0 ? last_wg / kKeys + 1 : 0;
+
+  TileLoad<P, kKeys, NW> lk, lv;
+  lk.init(wave, lane, a.ldk_t, a.D);
+  lv.init(wave, lane, a.ldv_t, a.D);
+  auto issue = [&](int t, int buf) {
+    uint8_t *at = smem + buf * 2 * kTile;
+    const int64_t row = (int64_t)t * kKeys;
+    lk.issue(k + row * a.ldk_t, sk.n - t * kKeys, at, wave);
+    lv.issue(v + row * a.ldv_t, sk.n - t * kKeys, at + kTile, wave);
+  };
+
+  const float scale2 = a.scale * kLog2e;  // exp(scale s) = 2^(scale2 s)
+  float top = -INFINITY, total = 0.0f;    // running maximum of s (both halves of a column), sum (this lane's)
+  f32x16 O[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) O[d] = zeros16();
+
+  if (tiles > 0) issue(0, 0);
+  for (int t = 0; t < tiles; ++t) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
+    const int key0 = t * kKeys;
+    if (key0 > last_wave) continue;
+    const uint8_t *tk = smem + (t & 1) * 2 * kTile, *tv = tk + kTile;
+
+    f32x16 S[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      S[i] = zeros16();
+#pragma unroll
+      for (int s = 0; s < KS; ++s) S[i] = mfma(read_rows<P>(tk, 32 * i, s, lane), Q[s], S[i]);
+    }
+    const bool masked = key0 + kKeys - 1 > first_limit;
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[i][r] = key0 + 32 * i + c_row(r, h) <= limit ? S[i][r] : -INFINITY;
+    }
+    float m = S[0][0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) m = fmaxf(m, S[0][r]);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) m = fmaxf(m, S[1][r]);
+    m = max_halves(m);
+    // The sums are kept relative to a maximum that may lag by 2^8: they cannot overflow, and are as exact.
+    if (__ballot((m - top) * scale2 > 8.0f)) {
+      const float next = fmaxf(top, m), old = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((top - next) * scale2);
+      top = next;
+      total *= old;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) O[d] *= old;
+    }
+    const float shift = top == -INFINITY ? 0.0f : top * scale2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        S[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i][r], scale2, -shift));
+        total += S[i][r];
+      }
+    const bool apart = masked && tile_nonfinite<P, kKeys>(tv, lane);
+    // rounding the exponentials to bf16 is what the matrix instruction takes: 2^-9 of each, averaged out
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bf16x8 p = as_operand(S[i], s);
+        const int r0 = 32 * i + 16 * s;
+        if (!apart) {
+#pragma unroll
+          for (int d = 0; d < DB; ++d) O[d] = mfma(read_columns<P>(tv, r0, d, lane), p, O[d]);
+        } else {
+          add_rows_apart<P, DB>(tv, r0, p, O, lane, [&](int row) { return key0 + row <= limit; });
+        }
+      }
+  }
+
+  total = add_halves(total);
+  if (query >= sq.n) return;
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // a query without keys: 0
+  uint16_t *out = static_cast<uint16_t *>(a.out) + (int64_t)(sq.begin + query) * a.ldo_t + head * a.ldo_h;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int at = 32 * d + 8 * g + 4 * h;
+      if (at >= a.D) continue;
+      const bf16x2 lo = {(__bf16)(O[d][4 * g] * inv), (__bf16)(O[d][4 * g + 1] * inv)};
+      const bf16x2 hi = {(__bf16)(O[d][4 * g + 2] * inv), (__bf16)(O[d][4 * g + 3] * inv)};
+      *reinterpret_cast<u32x2 *>(out + at) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    }
+  if (a.lse && h == 0)
+    a.lse[(int64_t)head * a.Tq + sq.begin + query] =
+        total == 0.0f ? -INFINITY : (top * scale2 + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+template <int KS, int DB, int NW>
+hipError_t launch(AttentionArgs a, hipStream_t stream) {
+  constexpr int kLds = 4 * kKeys * DB * 64;
+  static std::atomic<bool> done[kMaxDevices];
+  const void *kern = reinterpret_cast<const void *>(&k_attention<KS, DB, NW>);
+  if (hipError_t e = set_dynamic_lds(kern, kLds, done); e != hipSuccess) return e;
+  a.slots = (int)attention_slots(a.Tq, a.B, a.cu_q != nullptr, 32 * NW);
+  k_attention<KS, DB, NW><<<dim3((unsigned)(a.slots * a.Hq)), dim3(64 * NW), kLds, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int KS, int DB>
+hipError_t launch_waves(const AttentionArgs &a, hipStream_t stream) {
+  return launch<KS, DB, 4>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_attention(const AttentionArgs &a, hipStream_t stream) {
+  if (a.D <= 32) return launch_waves<2, 1>(a, stream);
+  if (a.D <= 64) return launch_waves<4, 2>(a, stream);
+  if (a.D <= 80) return launch_waves<5, 3>(a, stream);
+  if (a.D <= 96) return launch_waves<6, 3>(a, stream);
+  if (a.D <= 112) return launch_waves<7, 4>(a, stream);
+  return launch_waves<8, 4>(a, stream);
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,195 @@
+// What the attention kernels share (gfx950): sequences, tiles of head rows in LDS, matrix operands.
+//
+// All products are v_mfma_f32_32x32x16_bf16: C[32][32] += A[32][16] B[16][32].  Lane l = 32 h + c holds
+//   A   row c,     k = 8 h .. 8 h + 7        B   column c,  k = 8 h .. 8 h + 7
+//   C   column c,  rows 8 g + 4 h + i        (register 4 g + i; g, i = 0 .. 3)
+// So a lane's C registers 8 s .. 8 s + 7 are 8 rows of its column, and rounded to bf16 they are a B operand
+// over the k order  kappa(s, h, e) = 16 s + 8 (e / 4) + 4 h + e % 4:  the result of one product is the
+// operand of the next without a move between lanes, as long as its A operand lists k in the same order.
+#pragma once
+#include "launch.hpp"
+
+namespace nvfp4 {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// ---- sequences ----------------------------------------------------------------------------------------
+
+// Rows of a sequence; whatever the offsets hold, inside [0, T).
+struct SeqRows {
+  int begin, n;
+};
+__device__ __forceinline__ SeqRows seq_rows(const int32_t *cu, int b, int T, int per) {
+  if (!cu) return {b * per, per};
+  const int lo = min(max(cu[b], 0), T), hi = min(max(cu[b + 1], lo), T);
+  return {lo, hi - lo};
+}
+
+// Blocks of BLK rows of packed sequences are numbered by slots: sequence b's begin at cu[b] / BLK + b, which
+// leaves it at least ceil(n / BLK) of them, so a block finds its sequence by a search, and nobody has to
+// know the lengths on the host.  (Equal sequences, cu == NULL: per / BLK rounded up for each.)
+inline int64_t attention_slots(int64_t T, int64_t B, bool packed, int blk) {
+  return packed ? T / blk + B : B * ((T / (B > 0 ? B : 1) + blk - 1) / blk);
+}
+template <int BLK>
+__device__ __forceinline__ void find_block(int slot, const int32_t *cu, int B, int T, int per, int lane, int &b, int &blk) {
+  if (!cu) {
+    const int each = (per + BLK - 1) / BLK;
+    b = slot / each;
+    blk = slot - b * each;
+    return;
+  }
+  int lo = 0, len = B;  // the last b with cu[b] / BLK + b <= slot: 64 candidates at a time
+  while (len > 1) {
+    const int step = (len + 63) >> 6, at = lane * step;
+    const bool here = at < len && min(max(cu[lo + min(at, len - 1)], 0), T) / BLK + lo + at <= slot;
+    const int n = max((int)__popcll(__ballot(here)), 1);
+    lo += (n - 1) * step;
+    len = min(step, len - (n - 1) * step);
+  }
+  b = __builtin_amdgcn_readfirstlane(lo);
+  blk = slot - (min(max(cu[b], 0), T) / BLK + b);
+}
+
+// ---- tiles of head rows in LDS ------------------------------------------------------------------------
+//
+// A tile is ROWS rows of P 16-byte pieces, P = 4 DB (DB blocks of 32 values).  Piece p of row r lies in
+// place p ^ swizzle(r), so that both ways of reading it pass over all banks:
+//   by row       32 lanes the same piece of 32 rows (16 bytes each)
+//   transposed   16 lanes 4 rows of 32 bytes, two such groups side by side
+// P = 16: rows are 256 bytes, and r's low two bits have to move 64 bytes.  P = 8: rows 2 i and 2 i + 1
+// share 256 bytes.  P = 4, 12: four rows begin at four different 64 bytes already.
+template <int P>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (P == 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+  else if constexpr (P == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  else return (r >> 2) & 3;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void *base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, 0x7fffffff, 0x00027000);
+}
+constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer: loads give zeros
+
+// This lane's part of a tile's loads: NI wave-wide 16-byte LDS-DMAs, number j of all (j = wave + NW i) the
+// places 64 j .. 64 j + 63.
+template <int P, int ROWS, int NW>
+struct TileLoad {
+  static constexpr int kAll = ROWS * P / 64, kN = (kAll + NW - 1) / NW, kBytes = ROWS * P * 16;
+  uint32_t off[kN];
+  int row[kN];
+  __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int D) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int n = (wave + NW * i) * 64 + lane, r = n / P, p = (n - r * P) ^ swizzle<P>(r);
+      row[i] = r;
+      off[i] = p < D / 8 ? (uint32_t)r * (uint32_t)ld * 2u + 16u * p : kOutside;
+    }
+  }
+  // rows past `left` and pieces past D become zeros
+  __device__ __forceinline__ void issue(const uint16_t *base, int left, uint8_t *lds, int wave) const {
+    const __amdgpu_buffer_rsrc_t rsrc = row_buffer(base);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int j = wave + NW * i;
+      if (kAll % NW != 0 && j >= kAll) break;
+      const uint32_t o = row[i] < left ? off[i] : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t *)(lds + 1024 * j), 16, o, 0, 0, 0);
+    }
+  }
+};
+
+// A operand, rows r0 .. r0 + 31, values 16 s .. 16 s + 15 of a tile.
+template <int P>
+__device__ __forceinline__ bf16x8 read_rows(const uint8_t *tile, int r0, int s, int lane) {
+  const int r = r0 + (lane & 31);
+  return *reinterpret_cast<const bf16x8 *>(tile + r * (P * 16) + (((2 * s + (lane >> 5)) ^ swizzle<P>(r)) << 4));
+}
+// A operand of the transposed tile: rows are values 32 d .. 32 d + 31, k rows r0 + kappa(0, h, 0 .. 7) (r0 a
+// multiple of 16).  Each of the two reads turns 4 rows of 16 values per 16 lanes.
+template <int P>
+__device__ __forceinline__ bf16x8 read_columns(const uint8_t *tile, int r0, int d, int lane) {
+  const int i = lane & 15, r = r0 + 4 * (lane >> 5) + (i >> 2);
+  const int p = 4 * d + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+  const uint8_t *at = tile + 8 * (i & 1);
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + r * (P * 16) + ((p ^ swizzle<P>(r)) << 4)));
+  const s16x4 b =
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + (r + 8) * (P * 16) + ((p ^ swizzle<P>(r + 8)) << 4)));
+  return __builtin_bit_cast(bf16x8, s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+}
+
+// B operand from global memory: column c is row c of [n][ld], zeros past row n - 1 and past D.
+__device__ __forceinline__ bf16x8 load_column_operand(const uint16_t *base, int64_t ld, int row, int n, int s, int D,
+                                                      int lane) {
+  const int d = 16 * s + 8 * (lane >> 5);
+  u32x4 w = {0, 0, 0, 0};
+  if (row < n && d < D) w = *reinterpret_cast<const u32x4 *>(base + (int64_t)row * ld + d);
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+__device__ __forceinline__ f32x16 mfma(const bf16x8 &a, const bf16x8 &b, const f32x16 &c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zeros16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0}; }
+
+// C registers 8 s .. 8 s + 7 as a B operand, rounded to bf16.
+__device__ __forceinline__ bf16x8 as_operand(const f32x16 &c, int s) {
+  bf16x8 o;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = (__bf16)c[8 * s + e];
+  return o;
+}
+// Row of C register r (kappa: the same as 16 s + .. for r = 8 s + e).
+__device__ __forceinline__ int c_row(int r, int h) { return (r & 3) + 8 * (r >> 2) + 4 * h; }
+
+// Over the two lanes that share a column.
+__device__ __forceinline__ float max_halves(float v) {
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+}
+__device__ __forceinline__ float add_halves(float v) {
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r.x) + __uint_as_float(r.y);
+}
+
+// Whether a tile holds an infinity or a NaN (every lane of the wave gets the answer).
+template <int P, int ROWS>
+__device__ __forceinline__ bool tile_nonfinite(const uint8_t *tile, int lane) {
+  bool bad = false;
+#pragma unroll 4
+  for (int i = 0; i < ROWS * P / 64; ++i) {
+    const u32x4 w = *reinterpret_cast<const u32x4 *>(tile + 16 * (64 * i + lane));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bad |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+  }
+  return __ballot(bad) != 0;
+}
+
+// c[d] += (rows r0 .. r0 + 15 of a tile)^T b where b is 0 at masked (row, column) places and the tile holds
+// infinities or NaN: one at a masked place must not reach the column (0 times it is NaN).  Each row is
+// multiplied alone and added only to the columns that see it.  sees(row): whether this lane's column does.
+template <int P, int DB, typename Sees>
+__device__ __forceinline__ void add_rows_apart(const uint8_t *tile, int r0, const bf16x8 &b, f32x16 (&c)[DB], int lane,
+                                               Sees sees) {
+#pragma unroll 1
+  for (int row = 0; row < 16; ++row) {
+    const int h = (row >> 2) & 1, e = 4 * (row >> 3) + (row & 3);  // kappa(0, h, e) = row
+    const bool add = sees(r0 + row);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+      const u32x4 w = __builtin_bit_cast(u32x4, read_columns<P>(tile, r0, d, lane));
+      u32x4 one;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) one[i] = (lane >> 5) == h && e >> 1 == i ? w[i] & (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
+      const f32x16 t = mfma(__builtin_bit_cast(bf16x8, one), b, zeros16());
+#pragma unroll
+      for (int r = 0; r < 16; ++r) c[d][r] = add ? c[d][r] + t[r] : c[d][r];
+    }
+  }
+}
+
+}  // namespace nvfp4

@@ -189,4 +189,21 @@ struct W4A8Args {  // w4a8.hip
 };
 hipError_t launch_w4a8(const W4A8Args &g, hipStream_t stream);
 
+// ---- attention --------------------------------------------------------------------------------------
+
+constexpr int64_t kAttentionMaxD = 128;
+struct AttentionArgs {  // attention.hip; all bf16 but lse; pitches in elements, of tokens (_t) and heads (_h)
+  const void *q, *k, *v;
+  int64_t ldq_t, ldq_h, ldk_t, ldk_h, ldv_t, ldv_h;
+  int Tq, Tk, Hq, group, D, B;  // group: query heads per key head
+  const int32_t *cu_q, *cu_k;   // [B + 1], or null: B sequences of per_q and per_k rows
+  int per_q, per_k, causal;
+  float scale;
+  void *out;
+  int64_t ldo_t, ldo_h;
+  float *lse;     // [Hq][Tq] or null
+  int slots = 0;  // blocks of rows; the launcher sets it
+};
+hipError_t launch_attention(const AttentionArgs &a, hipStream_t stream);
+
 }  // namespace nvfp4

@@ -1,0 +1,74 @@
+// libnvfp4 C ABI, attention: whole prompts and their gradients, a paged cache and single tokens over it.
+// Semantics and layouts are documented in include/nvfp4.h.
+#include "../../include/nvfp4.h"
+
+#include <cmath>
+
+#include "api_checks.hpp"
+#include "launch.hpp"
+
+using namespace nvfp4;
+
+namespace {
+
+constexpr int64_t kMaxPitch = (int64_t)1 << 23;  // offsets inside a tile of 64 rows fit 31 bits
+
+struct Heads {  // [T][H][D] bf16 at token and head pitches
+  const void *p;
+  int64_t T, H, ld_t, ld_h;
+};
+
+nvfp4_status_t check_heads(const Heads &x, int64_t D, bool written) {
+  if (x.T == 0 || x.H == 0) return NVFP4_OK;
+  if (!x.p) return NVFP4_ERR_NULL;
+  if (x.ld_t >= kMaxPitch || !head_rows_fit(x.T, x.H, D, x.ld_t, x.ld_h, written)) return NVFP4_ERR_STRIDE;
+  if (!rows_aligned(x.p, x.ld_t, NVFP4_BF16) || !rows_aligned(x.p, x.ld_h, NVFP4_BF16)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+// a written array at an input's address has its pitches
+bool same_place_fits(const Heads &out, const Heads &in) {
+  return out.p != in.p || ((out.T <= 1 || out.ld_t == in.ld_t) && (out.H <= 1 || out.ld_h == in.ld_h));
+}
+
+nvfp4_status_t check_attention_shape(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, const int32_t *cu_q,
+                                     const int32_t *cu_k, int64_t B, float scale) {
+  constexpr int64_t kRows = (int64_t)1 << 31;
+  if (Tq < 0 || Tk < 0 || Tq >= kRows || Tk >= kRows || Hq < 0 || Hkv < 0 || Hq > (1 << 16) || Hkv > Hq || D < 8 ||
+      D > kAttentionMaxD || D % 8 != 0 || B < 0 || B > (1 << 20) || (Hq > 0 && (Hkv == 0 || Hq % Hkv != 0)))
+    return NVFP4_ERR_SHAPE;
+  if ((cu_q == nullptr) != (cu_k == nullptr)) return NVFP4_ERR_NULL;
+  if (!cu_q && B > 0 && (Tq % B != 0 || Tk % B != 0)) return NVFP4_ERR_SHAPE;
+  // at most a workgroup of 512 threads per head and 32 rows, and 2^32 threads
+  if (((Tq > Tk ? Tq : Tk) / 32 + B + 1) * Hq >= ((int64_t)1 << 23)) return NVFP4_ERR_SHAPE;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return NVFP4_ERR_MODE;
+  if (!aligned(cu_q, 4) || !aligned(cu_k, 4)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_head, const void *k, int64_t ldk_token,
+                               int64_t ldk_head, const void *v, int64_t ldv_token, int64_t ldv_head, int64_t Tq,
+                               int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, const int32_t *cu_q,
+                               const int32_t *cu_k, int64_t B, int causal, float scale, void *out, int64_t ldo_token,
+                               int64_t ldo_head, float *lse, void *stream) {
+  nvfp4_status_t st = check_attention_shape(Tq, Tk, Hq, Hkv, D, cu_q, cu_k, B, scale);
+  if (st != NVFP4_OK) return st;
+  if (Tq == 0 || Hq == 0 || B == 0) return NVFP4_OK;
+  const Heads hq{q, Tq, Hq, ldq_token, ldq_head}, hk{k, Tk, Hkv, ldk_token, ldk_head}, hv{v, Tk, Hkv, ldv_token, ldv_head},
+      ho{out, Tq, Hq, ldo_token, ldo_head};
+  if ((st = check_heads(hq, D, false)) != NVFP4_OK || (st = check_heads(hk, D, false)) != NVFP4_OK ||
+      (st = check_heads(hv, D, false)) != NVFP4_OK || (st = check_heads(ho, D, true)) != NVFP4_OK)
+    return st;
+  if (!same_place_fits(ho, hq)) return NVFP4_ERR_STRIDE;
+  if (!aligned(lse, 4)) return NVFP4_ERR_ALIGN;
+  if ((st = check_device()) != NVFP4_OK) return st;
+  const AttentionArgs a{q, k, v, ldq_token, ldq_head, ldk_token, ldk_head, ldv_token, ldv_head, (int)Tq, (int)Tk, (int)Hq,
+                        (int)(Hq / Hkv), (int)D, (int)B, cu_q, cu_k, (int)(Tq / B), (int)(Tk / B), causal != 0, scale, out,
+                        ldo_token, ldo_head, lse};
+  return hip_status(launch_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
