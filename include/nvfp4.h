@@ -488,6 +488,27 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
                                const int32_t *cu_k, int64_t B, int causal, float scale, void *out, int64_t ldo_token,
                                int64_t ldo_head, float *lse, void *stream);
 
+/* Its gradients: from dout (the gradient of out) and out and lse as nvfp4_attention wrote them for the same
+ * q, k, v, sequences, causal and scale, with delta_i = dout_i . o_i, ds_ij = p_ij (dout_i . v_j - delta_i):
+ *     dq_i = scale sum_j ds_ij k_j     dv_j = sum_i p_ij dout_i     dk_j = scale sum_i ds_ij q_i
+ * dk and dv summed over the query heads that share a key head.  p and ds are rounded to bf16 for these
+ * products; the sums are fp32 and run in a fixed order: equal inputs give equal bits.
+ *   dout, out, dq   bf16 [Tq][Hq][D], dk, dv bf16 [Tk][Hkv][D], at their own pitches as above.
+ *   dq, dk, dv      written; at no input's address (NVFP4_ERR_STRIDE) and not overlapping any array.  Rows
+ *                   past the last sequence are left as they were; keys that nothing attends get 0.
+ *   workspace       nvfp4_attention_backward_workspace_bytes(Tq, Hq) bytes, 16-byte aligned, no initialization.
+ * B == 0 or Hq == 0 is valid and touches nothing; Tq == 0 writes dk = dv = 0. */
+size_t nvfp4_attention_backward_workspace_bytes(int64_t Tq, int64_t Hq);
+nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, int64_t lddo_head, const void *q,
+                                        int64_t ldq_token, int64_t ldq_head, const void *k, int64_t ldk_token,
+                                        int64_t ldk_head, const void *v, int64_t ldv_token, int64_t ldv_head,
+                                        const void *out, int64_t ldo_token, int64_t ldo_head, const float *lse,
+                                        int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
+                                        const int32_t *cu_q, const int32_t *cu_k, int64_t B, int causal, float scale,
+                                        void *dq, int64_t lddq_token, int64_t lddq_head, void *dk, int64_t lddk_token,
+                                        int64_t lddk_head, void *dv, int64_t lddv_token, int64_t lddv_head,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -51,7 +51,7 @@ EXPORTED = (
     "nvfp4_quantize_noalloc", "nvfp4_set_debug_checks",
     "nvfp4_mx8_quantize", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes", "nvfp4_rmsnorm_backward",
     "nvfp4_mx_gemm_w4a8", "nvfp4_rope_axes",
-    "nvfp4_attention",
+    "nvfp4_attention", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward",
 )
 
 _lib = None
@@ -147,6 +147,11 @@ def lib():
     heads = [_vp, _i64, _i64]  # address, token pitch, head pitch
     L.nvfp4_attention.restype = _i
     L.nvfp4_attention.argtypes = heads * 3 + [_i64] * 5 + [_vp, _vp, _i64, _i, ctypes.c_float] + heads + [_vp, _vp]
+    L.nvfp4_attention_backward_workspace_bytes.restype = _sz
+    L.nvfp4_attention_backward_workspace_bytes.argtypes = [_i64, _i64]
+    L.nvfp4_attention_backward.restype = _i
+    L.nvfp4_attention_backward.argtypes = heads * 5 + [_vp] + [_i64] * 5 + [_vp, _vp, _i64, _i, ctypes.c_float] + \
+        heads * 3 + [_vp, _sz, _vp]
     _lib = L
     return L
 
@@ -878,6 +883,77 @@ def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal
     return out, lse
 
 
+def nvfp4_attention_backward_workspace_bytes(Tq: int, Hq: int) -> int:
+    return int(lib().nvfp4_attention_backward_workspace_bytes(Tq, Hq))
+
+
+def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                             lse: torch.Tensor, *, causal: bool = False, scale: float | None = None,
+                             cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, batch: int = 1,
+                             dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of nvfp4_attention from dout (the gradient of out), its inputs, its out and its lse, with the same
+    sequences, causal and scale.  Returns (dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]), bf16; rows past the last sequence are 0 in
+    new tensors and left as they were in given ones (any strides as for q; not an input's memory)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_attention_backward(dout, q, k, v, out, lse, causal=causal, scale=scale, cu_q=cu_q, cu_k=cu_k,
+                                            batch=batch, dq=dq, dk=dk, dv=dv, workspace=workspace)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [T, H, D]")
+    Tq, Hq, D = shape_q = q.shape
+    Tk, Hkv, _ = k.shape
+    shape_k = (Tk, Hkv, D)
+    dev = _launch_device(q)
+    args = [*_heads(dout, "dout", shape_q, dev), *_heads(q, "q", shape_q, dev), *_heads(k, "k", shape_k, dev),
+            *_heads(v, "v", shape_k, dev), *_heads(out, "out", shape_q, dev), _dense(lse, "lse", (Hq, Tq), _f32, dev)]
+    p_cq, p_ck, batch = _offsets(cu_q, cu_k, batch, dev)
+    grads = []
+    for t, name, shape in ((dq, "dq", shape_q), (dk, "dk", shape_k), (dv, "dv", shape_k)):
+        if t is None:
+            t = (torch.empty if p_cq == 0 else torch.zeros)(shape, dtype=_bf16, device=q.device)
+        else:
+            _heads(t, name, shape, dev)
+            _written(t, name)
+        grads.append(t)
+    L = lib()
+    if workspace is None:
+        n = L.nvfp4_attention_backward_workspace_bytes(Tq, Hq)
+        workspace = torch.empty(n, dtype=_u8, device=q.device)
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, not on {q.device}")
+    else:
+        n = workspace.numel() * workspace.element_size()
+    st = L.nvfp4_attention_backward(*args, Tq, Tk, Hq, Hkv, D, p_cq, p_ck, batch, 1 if causal else 0,
+                                    D ** -0.5 if scale is None else scale, *_heads(grads[0], "dq", shape_q, dev),
+                                    *_heads(grads[1], "dk", shape_k, dev), *_heads(grads[2], "dv", shape_k, dev),
+                                    workspace.data_ptr(), n, _current_stream(dev))
+    if st:
+        raise NVFP4Error(st, "nvfp4_attention_backward")
+    return tuple(grads)
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_q, cu_k, how):
+        q, k, v = _heads_of(q), _heads_of(k), _heads_of(v)
+        out, lse = nvfp4_attention(q, k, v, cu_q=cu_q, cu_k=cu_k, save_lse=True, **how)
+        ctx.save_for_backward(q, k, v, out, lse, cu_q, cu_k)
+        ctx.how = how
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse, cu_q, cu_k = ctx.saved_tensors
+        return *nvfp4_attention_backward(_heads_of(dout), q, k, v, out, lse, cu_q=cu_q, cu_k=cu_k, **ctx.how), None, None, None
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False, scale: float | None = None,
+              cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, batch: int = 1) -> torch.Tensor:
+    """Differentiable nvfp4_attention of tensors in any strides: out [Tq, Hq, D]."""
+    return _Attention.apply(q, k, v, cu_q, cu_k, dict(causal=causal, scale=scale, batch=batch))
+
+
 __all__ = [
     "Status", "NVFP4Error", "lib", "LIB_PATH", "EXPORTED", "F32", "BF16", "W4A4", "W4A16",
     "SCALE_DYNAMIC", "SCALE_STATIC", "nvfp4_set_debug_checks",
@@ -891,5 +967,5 @@ __all__ = [
     "nvfp4_mx8_quantize", "RMSNormOutput", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes",
     "nvfp4_rmsnorm_backward", "rmsnorm", "nvfp4_mx_gemm_w4a8",
     "ROPE_PAIRS", "ROPE_HALVES", "rope_inv_freq", "nvfp4_rope_axes", "rope_axes",
-    "nvfp4_attention",
+    "nvfp4_attention", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward", "attention",
 ]

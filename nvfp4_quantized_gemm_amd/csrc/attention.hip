@@ -106,9 +106,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     for (int r = 0; r < 16; ++r) m = fmaxf(m, S[1][r]);
     m = max_halves(m);
     // The sums are kept relative to a maximum that may lag by 2^8: they cannot overflow, and are as exact.
-    if (__ballot((m - top) * scale2 > 8.0f)) {
-      const float next = fmaxf(top, m), old = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((top - next) * scale2);
-      top = next;
+    // Only the queries that need it move theirs, so that a query's bits do not depend on its neighbours.
+    const bool rise = (m - top) * scale2 > 8.0f;
+    if (__ballot(rise)) {
+      const float old = !rise ? 1.0f : top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((top - m) * scale2);
+      top = rise ? m : top;
       total *= old;
 #pragma unroll
       for (int d = 0; d < DB; ++d) O[d] *= old;
@@ -142,16 +144,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   if (query >= sq.n) return;
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // a query without keys: 0
   uint16_t *out = static_cast<uint16_t *>(a.out) + (int64_t)(sq.begin + query) * a.ldo_t + head * a.ldo_h;
-#pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int at = 32 * d + 8 * g + 4 * h;
-      if (at >= a.D) continue;
-      const bf16x2 lo = {(__bf16)(O[d][4 * g] * inv), (__bf16)(O[d][4 * g + 1] * inv)};
-      const bf16x2 hi = {(__bf16)(O[d][4 * g + 2] * inv), (__bf16)(O[d][4 * g + 3] * inv)};
-      *reinterpret_cast<u32x2 *>(out + at) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-    }
+  store_column<DB>(O, inv, out, a.D, h);
   if (a.lse && h == 0)
     a.lse[(int64_t)head * a.Tq + sq.begin + query] =
         total == 0.0f ? -INFINITY : (top * scale2 + __builtin_amdgcn_logf(total)) * kLn2;

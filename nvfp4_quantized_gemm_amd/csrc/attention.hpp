@@ -146,6 +146,21 @@ __device__ __forceinline__ bf16x8 as_operand(const f32x16 &c, int s) {
 // Row of C register r (kappa: the same as 16 s + .. for r = 8 s + e).
 __device__ __forceinline__ int c_row(int r, int h) { return (r & 3) + 8 * (r >> 2) + 4 * h; }
 
+// Column c of a result C^T (rows are the D values of a head) to row `out` of a bf16 tensor, times f.
+template <int DB>
+__device__ __forceinline__ void store_column(const f32x16 (&c)[DB], float f, uint16_t *out, int D, int h) {
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int at = 32 * d + 8 * g + 4 * h;
+      if (at >= D) continue;
+      const bf16x2 lo = {(__bf16)(c[d][4 * g] * f), (__bf16)(c[d][4 * g + 1] * f)};
+      const bf16x2 hi = {(__bf16)(c[d][4 * g + 2] * f), (__bf16)(c[d][4 * g + 3] * f)};
+      *reinterpret_cast<u32x2 *>(out + at) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    }
+}
+
 // Over the two lanes that share a column.
 __device__ __forceinline__ float max_halves(float v) {
   const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -170,24 +185,36 @@ __device__ __forceinline__ bool tile_nonfinite(const uint8_t *tile, int lane) {
 }
 
 // c[d] += (rows r0 .. r0 + 15 of a tile)^T b where b is 0 at masked (row, column) places and the tile holds
-// infinities or NaN: one at a masked place must not reach the column (0 times it is NaN).  Each row is
-// multiplied alone and added only to the columns that see it.  sees(row): whether this lane's column does.
+// infinities or NaN: one at a masked place must not reach the column (0 times it is NaN).  The finite values
+// are multiplied as always, so what no other value touches has the same bits; then the others, each row
+// alone, added only to the columns that see it.  sees(row): whether this lane's column does.
 template <int P, int DB, typename Sees>
 __device__ __forceinline__ void add_rows_apart(const uint8_t *tile, int r0, const bf16x8 &b, f32x16 (&c)[DB], int lane,
                                                Sees sees) {
+  auto split = [](uint32_t w, bool finite) {  // the halves of w that are finite, or those that are not
+    const uint32_t bad = ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+    return finite ? w & ~bad : w & bad;
+  };
+#pragma unroll
+  for (int d = 0; d < DB; ++d) {
+    u32x4 w = __builtin_bit_cast(u32x4, read_columns<P>(tile, r0, d, lane));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = split(w[i], true);
+    c[d] = mfma(__builtin_bit_cast(bf16x8, w), b, c[d]);
+  }
 #pragma unroll 1
   for (int row = 0; row < 16; ++row) {
     const int h = (row >> 2) & 1, e = 4 * (row >> 3) + (row & 3);  // kappa(0, h, e) = row
     const bool add = sees(r0 + row);
 #pragma unroll
     for (int d = 0; d < DB; ++d) {
-      const u32x4 w = __builtin_bit_cast(u32x4, read_columns<P>(tile, r0, d, lane));
-      u32x4 one;
+      u32x4 w = __builtin_bit_cast(u32x4, read_columns<P>(tile, r0, d, lane));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) one[i] = (lane >> 5) == h && e >> 1 == i ? w[i] & (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
-      const f32x16 t = mfma(__builtin_bit_cast(bf16x8, one), b, zeros16());
+      for (int i = 0; i < 4; ++i)
+        w[i] = (lane >> 5) == h && e >> 1 == i ? split(w[i], false) & (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
+      const f32x16 t = mfma(__builtin_bit_cast(bf16x8, w), b, zeros16());
 #pragma unroll
-      for (int r = 0; r < 16; ++r) c[d][r] = add ? c[d][r] + t[r] : c[d][r];
+      for (int r = 0; r < 16; ++r) c[d][r] = add && t[r] != 0.0f ? c[d][r] + t[r] : c[d][r];
     }
   }
 }

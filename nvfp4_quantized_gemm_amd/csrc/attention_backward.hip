@@ -1,0 +1,310 @@
+// Gradients of softmax attention (gfx950).  With P_ij = exp(scale q_i k_j - lse_i), delta_i = sum dO_i O_i,
+// dS_ij = P_ij (dO_i v_j - delta_i):
+//   dQ_i = scale sum_j dS_ij k_j     dV_j = sum_i P_ij dO_i     dK_j = scale sum_i dS_ij q_i
+// with sums over the query heads that share a key head.
+//
+// Two kernels, one with queries as the columns of its products (as forward) for dQ, one with keys as columns
+// for dK and dV: each gradient is summed in one wave's registers in a fixed order, without atomics, for
+// computing scores and dO V^T twice (seven products instead of five).  P and dS are rounded to bf16 where
+// they are multiplied; everything else is fp32.
+#include "attention.hpp"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kRows = 64;  // rows per tile
+
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Heads of the innermost grid: see k_attention.
+__device__ __forceinline__ void block_of(int heads, int slots, bool slots_first, int &head, int &slot) {
+  const bool own = heads % 8 == 0;
+  const int w = blockIdx.x, per = own ? heads / 8 : heads, i = own ? w >> 3 : w, x = own ? (w & 7) * per : 0;
+  if (slots_first) {
+    slot = i / per;
+    head = x + i % per;
+  } else {
+    head = x + i / slots;
+    slot = i % slots;
+  }
+}
+
+template <int KS, int DB, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attention_dq(const AttentionGradArgs g) {
+  const AttentionArgs &a = g.f;
+  constexpr int P = 4 * DB, BQ = 32 * NW, kTile = kRows * P * 16;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int head, slot, b, blk;
+  block_of(a.Hq, a.slots, a.causal, head, slot);
+  if (a.causal) slot = a.slots - 1 - slot;
+  find_block<BQ>(slot, a.cu_q, a.B, a.Tq, a.per_q, lane, b, blk);
+  const SeqRows sq = seq_rows(a.cu_q, b, a.Tq, a.per_q), sk = seq_rows(a.cu_k, b, a.Tk, a.per_k);
+  if (blk < 0 || blk * BQ >= sq.n) return;
+  const int kv = head / a.group, q0 = blk * BQ + 32 * wave, query = q0 + c, ahead = sk.n - sq.n;
+
+  const uint16_t *q = static_cast<const uint16_t *>(a.q) + sq.begin * a.ldq_t + head * a.ldq_h;
+  const uint16_t *k = static_cast<const uint16_t *>(a.k) + sk.begin * a.ldk_t + kv * a.ldk_h;
+  const uint16_t *v = static_cast<const uint16_t *>(a.v) + sk.begin * a.ldv_t + kv * a.ldv_h;
+  const uint16_t *dout = static_cast<const uint16_t *>(g.dout) + sq.begin * g.lddo_t + head * g.lddo_h;
+  const uint16_t *out = static_cast<const uint16_t *>(a.out) + sq.begin * a.ldo_t + head * a.ldo_h;
+  bf16x8 Q[KS], dO[KS];
+  float delta = 0.0f;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    Q[s] = load_column_operand(q, a.ldq_t, query, sq.n, s, a.D, lane);
+    dO[s] = load_column_operand(dout, g.lddo_t, query, sq.n, s, a.D, lane);
+    const bf16x8 o = load_column_operand(out, a.ldo_t, query, sq.n, s, a.D, lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)dO[s][e], (float)o[e], delta);
+  }
+  delta = add_halves(delta);
+  const int64_t at = (int64_t)head * a.Tq + sq.begin + query;
+  const float lse2 = query < sq.n ? a.lse[at] * kLog2e : 0.0f;
+  if (query < sq.n && h == 0) {
+    g.rows[at] = lse2;
+    g.rows[(int64_t)a.Hq * a.Tq + at] = delta;
+  }
+
+  const int limit = a.causal ? min(query + ahead, sk.n - 1) : sk.n - 1;
+  const int last_wg = a.causal ? min(min((blk + 1) * BQ, sq.n) - 1 + ahead, sk.n - 1) : sk.n - 1;
+  const int last_wave = a.causal ? min(q0 + 31 + ahead, sk.n - 1) : sk.n - 1;
+  const int first_limit = a.causal ? min(q0 + ahead, sk.n - 1) : sk.n - 1;
+  const int tiles = last_wg >= 0 ? last_wg / kRows + 1 : 0;
+  TileLoad<P, kRows, NW> lk, lv;
+  lk.init(wave, lane, a.ldk_t, a.D);
+  lv.init(wave, lane, a.ldv_t, a.D);
+  auto issue = [&](int t, int buf) {
+    uint8_t *to = smem + buf * 2 * kTile;
+    const int64_t row = (int64_t)t * kRows;
+    lk.issue(k + row * a.ldk_t, sk.n - t * kRows, to, wave);
+    lv.issue(v + row * a.ldv_t, sk.n - t * kRows, to + kTile, wave);
+  };
+  const float scale2 = a.scale * kLog2e;
+  f32x16 dQ[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) dQ[d] = zeros16();
+
+  if (tiles > 0) issue(0, 0);
+  for (int t = 0; t < tiles; ++t) {
+    tile_barrier();
+    if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
+    const int key0 = t * kRows;
+    if (key0 > last_wave) continue;
+    const uint8_t *tk = smem + (t & 1) * 2 * kTile, *tv = tk + kTile;
+    const bool masked = key0 + kRows - 1 > first_limit;
+    const bool apart = masked && tile_nonfinite<P, kRows>(tk, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f32x16 S = zeros16(), dP = zeros16();
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        S = mfma(read_rows<P>(tk, 32 * i, s, lane), Q[s], S);
+        dP = mfma(read_rows<P>(tv, 32 * i, s, lane), dO[s], dP);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        S[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], scale2, -lse2)) * (dP[r] - delta);
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[r] = key0 + 32 * i + c_row(r, h) <= limit ? S[r] : 0.0f;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bf16x8 ds = as_operand(S, s);
+        const int r0 = 32 * i + 16 * s;
+        if (!apart) {
+#pragma unroll
+          for (int d = 0; d < DB; ++d) dQ[d] = mfma(read_columns<P>(tk, r0, d, lane), ds, dQ[d]);
+        } else {
+          add_rows_apart<P, DB>(tk, r0, ds, dQ, lane, [&](int row) { return key0 + row <= limit; });
+        }
+      }
+    }
+  }
+  if (query >= sq.n) return;
+  store_column<DB>(dQ, a.scale, static_cast<uint16_t *>(g.dq) + (int64_t)(sq.begin + query) * g.lddq_t + head * g.lddq_h, a.D, h);
+}
+
+// KW waves of 32 keys; RS waves take turns at the 32-row halves of a tile, and their sums are added at the end.
+template <int KS, int DB, int KW, int RS>
+__global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(RS, RS))) void k_attention_dkv(const AttentionGradArgs g) {
+  const AttentionArgs &a = g.f;
+  constexpr int P = 4 * DB, BK = 32 * KW, NW = KW * RS, kTile = kRows * P * 16, kStage = 2 * kTile + 2 * kRows * 4;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kw = wave % KW, rs = wave / KW;
+  int kv, slot, b, blk;
+  block_of(a.Hq / a.group, a.slots, a.causal, kv, slot);
+  find_block<BK>(slot, a.cu_k, a.B, a.Tk, a.per_k, lane, b, blk);
+  const SeqRows sq = seq_rows(a.cu_q, b, a.Tq, a.per_q), sk = seq_rows(a.cu_k, b, a.Tk, a.per_k);
+  if (blk < 0 || blk * BK >= sk.n) return;
+  const int k0 = blk * BK + 32 * kw, key = k0 + c, ahead = sk.n - sq.n;
+  const uint16_t *k = static_cast<const uint16_t *>(a.k) + sk.begin * a.ldk_t + kv * a.ldk_h;
+  const uint16_t *v = static_cast<const uint16_t *>(a.v) + sk.begin * a.ldv_t + kv * a.ldv_h;
+  bf16x8 K[KS], V[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    K[s] = load_column_operand(k, a.ldk_t, key, sk.n, s, a.D, lane);
+    V[s] = load_column_operand(v, a.ldv_t, key, sk.n, s, a.D, lane);
+  }
+  // the first query that attends a key j is j - ahead
+  const int first_row = a.causal ? key - ahead : 0;
+  const int last_first = a.causal ? k0 + 31 - ahead : 0, first_wave = a.causal ? max(k0 - ahead, 0) : 0;
+  const int first_tile = (a.causal ? max(blk * BK - ahead, 0) : 0) / kRows, tiles = (sq.n + kRows - 1) / kRows;
+  const int steps = tiles > first_tile ? (tiles - first_tile) * a.group : 0;
+
+  TileLoad<P, kRows, NW> lq, lo;
+  lq.init(wave, lane, a.ldq_t, a.D);
+  lo.init(wave, lane, g.lddo_t, a.D);
+  int ih = 0, it = first_tile;  // the next step to load: head of the group, tile
+  auto issue = [&](int buf) {
+    uint8_t *to = smem + buf * kStage;
+    const int head = kv * a.group + ih;
+    const int64_t row = sq.begin + (int64_t)it * kRows;
+    const int left = sq.n - it * kRows;
+    lq.issue(static_cast<const uint16_t *>(a.q) + row * a.ldq_t + head * a.ldq_h, left, to, wave);
+    lo.issue(static_cast<const uint16_t *>(g.dout) + row * g.lddo_t + head * g.lddo_h, left, to + kTile, wave);
+    if (wave < 2) {  // the rows' log sums, and their sums of dO O
+      const float *rows = g.rows + ((int64_t)wave * a.Hq + head) * a.Tq + row;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(rows), (lds_void_t *)(to + 2 * kTile + wave * kRows * 4), 4,
+                                               lane < left ? 4 * lane : kOutside, 0, 0, 0);
+    }
+    if (++it == tiles) {
+      it = first_tile;
+      ++ih;
+    }
+  };
+  const float scale2 = a.scale * kLog2e;
+  f32x16 dK[DB], dV[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) dK[d] = dV[d] = zeros16();
+
+  if (steps > 0) issue(0);
+  int t = first_tile;
+  for (int step = 0; step < steps; ++step) {
+    tile_barrier();
+    if (step + 1 < steps) issue((step + 1) & 1);
+    const uint8_t *tq = smem + (step & 1) * kStage, *to = tq + kTile;
+    const float *rows = reinterpret_cast<const float *>(tq + 2 * kTile);
+    const int tile0 = t * kRows;
+    t = t + 1 == tiles ? first_tile : t + 1;
+    const bool masked = tile0 < last_first;
+    if (tile0 + kRows - 1 < first_wave) continue;
+    const bool apart = masked && (tile_nonfinite<P, kRows>(tq, lane) || tile_nonfinite<P, kRows>(to, lane));
+#pragma unroll
+    for (int j = 0; j < 2 / RS; ++j) {
+      const int i = RS == 2 ? rs : j, row0 = tile0 + 32 * i;
+      f32x16 S = zeros16(), dP = zeros16();
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        S = mfma(read_rows<P>(tq, 32 * i, s, lane), K[s], S);
+        dP = mfma(read_rows<P>(to, 32 * i, s, lane), V[s], dP);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(rows + 32 * i + 8 * u + 4 * h);
+        const f32x4 delta = *reinterpret_cast<const f32x4 *>(rows + kRows + 32 * i + 8 * u + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          S[4 * u + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * u + e], scale2, -lse2[e]));
+          dP[4 * u + e] = S[4 * u + e] * (dP[4 * u + e] - delta[e]);
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const bool in = row0 + c_row(r, h) >= first_row;
+          S[r] = in ? S[r] : 0.0f;
+          dP[r] = in ? dP[r] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bf16x8 p = as_operand(S, s), ds = as_operand(dP, s);
+        const int r0 = 32 * i + 16 * s;
+        if (!apart) {
+#pragma unroll
+          for (int d = 0; d < DB; ++d) {
+            dV[d] = mfma(read_columns<P>(to, r0, d, lane), p, dV[d]);
+            dK[d] = mfma(read_columns<P>(tq, r0, d, lane), ds, dK[d]);
+          }
+        } else {
+          add_rows_apart<P, DB>(to, r0, p, dV, lane, [&](int row) { return tile0 + row >= first_row; });
+          add_rows_apart<P, DB>(tq, r0, ds, dK, lane, [&](int row) { return tile0 + row >= first_row; });
+        }
+      }
+    }
+  }
+  if constexpr (RS == 2) {  // the second half's sums join the first's
+    f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + kw * (DB * 4 * 64) + lane;
+    auto join = [&](f32x16(&x)[DB]) {
+      __syncthreads();
+      if (rs == 1) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) part[(4 * d + u) * 64] = f32x4{x[d][4 * u], x[d][4 * u + 1], x[d][4 * u + 2], x[d][4 * u + 3]};
+      }
+      __syncthreads();
+      if (rs == 0) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const f32x4 o = part[(4 * d + u) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[d][4 * u + e] += o[e];
+          }
+      }
+    };
+    join(dK);
+    join(dV);
+    if (rs == 1) return;
+  }
+  if (key >= sk.n) return;
+  const int64_t row = sk.begin + key;
+  store_column<DB>(dK, a.scale, static_cast<uint16_t *>(g.dk) + row * g.lddk_t + kv * g.lddk_h, a.D, h);
+  store_column<DB>(dV, 1.0f, static_cast<uint16_t *>(g.dv) + row * g.lddv_t + kv * g.lddv_h, a.D, h);
+}
+
+template <int KS, int DB>
+hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
+  constexpr int NW = 4, KW = 4, RS = DB <= 3 ? 2 : 1;
+  constexpr int kTile = kRows * DB * 64, kLdsQ = 4 * kTile, kLdsK = 2 * (2 * kTile + 2 * kRows * 4);
+  static_assert(RS == 1 || KW * DB * 4096 <= kLdsK, "the sums pass through the tiles' memory");
+  static std::atomic<bool> done_q[kMaxDevices], done_k[kMaxDevices];
+  if (g.f.Tq > 0) {
+    const void *kern = reinterpret_cast<const void *>(&k_attention_dq<KS, DB, NW>);
+    if (hipError_t e = set_dynamic_lds(kern, kLdsQ, done_q); e != hipSuccess) return e;
+    g.f.slots = (int)attention_slots(g.f.Tq, g.f.B, g.f.cu_q != nullptr, 32 * NW);
+    k_attention_dq<KS, DB, NW><<<dim3((unsigned)(g.f.slots * g.f.Hq)), dim3(64 * NW), kLdsQ, stream>>>(g);
+  }
+  if (g.f.Tk > 0) {
+    const void *kern = reinterpret_cast<const void *>(&k_attention_dkv<KS, DB, KW, RS>);
+    if (hipError_t e = set_dynamic_lds(kern, kLdsK, done_k); e != hipSuccess) return e;
+    g.f.slots = (int)attention_slots(g.f.Tk, g.f.B, g.f.cu_k != nullptr, 32 * KW);
+    k_attention_dkv<KS, DB, KW, RS>
+        <<<dim3((unsigned)(g.f.slots * (g.f.Hq / g.f.group))), dim3(64 * KW * RS), kLdsK, stream>>>(g);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention_backward(const AttentionGradArgs &g, hipStream_t stream) {
+  const int D = g.f.D;
+  if (D <= 32) return launch<2, 1>(g, stream);
+  if (D <= 64) return launch<4, 2>(g, stream);
+  if (D <= 80) return launch<5, 3>(g, stream);
+  if (D <= 96) return launch<6, 3>(g, stream);
+  if (D <= 112) return launch<7, 4>(g, stream);
+  return launch<8, 4>(g, stream);
+}
+
+}  // namespace nvfp4

@@ -205,5 +205,14 @@ struct AttentionArgs {  // attention.hip; all bf16 but lse; pitches in elements,
   int slots = 0;  // blocks of rows; the launcher sets it
 };
 hipError_t launch_attention(const AttentionArgs &a, hipStream_t stream);
+struct AttentionGradArgs {  // attention_backward.hip
+  AttentionArgs f;          // out and lse as the forward call wrote them
+  const void *dout;
+  int64_t lddo_t, lddo_h;
+  void *dq, *dk, *dv;
+  int64_t lddq_t, lddq_h, lddk_t, lddk_h, lddv_t, lddv_h;
+  float *rows;  // workspace: [2][Hq][Tq], a query's log sum (base 2) and sum of dO O
+};
+hipError_t launch_attention_backward(const AttentionGradArgs &a, hipStream_t stream);
 
 }  // namespace nvfp4

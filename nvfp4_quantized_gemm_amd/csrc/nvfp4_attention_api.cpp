@@ -71,4 +71,45 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
   return hip_status(launch_attention(a, static_cast<hipStream_t>(stream)));
 }
 
+size_t nvfp4_attention_backward_workspace_bytes(int64_t Tq, int64_t Hq) {
+  if (Tq < 0 || Hq < 0 || Tq >= ((int64_t)1 << 31) || Hq > (1 << 16)) return 0;
+  return 2 * sizeof(float) * (size_t)Tq * (size_t)Hq;
+}
+
+nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, int64_t lddo_head, const void *q,
+                                        int64_t ldq_token, int64_t ldq_head, const void *k, int64_t ldk_token,
+                                        int64_t ldk_head, const void *v, int64_t ldv_token, int64_t ldv_head,
+                                        const void *out, int64_t ldo_token, int64_t ldo_head, const float *lse,
+                                        int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
+                                        const int32_t *cu_q, const int32_t *cu_k, int64_t B, int causal, float scale,
+                                        void *dq, int64_t lddq_token, int64_t lddq_head, void *dk, int64_t lddk_token,
+                                        int64_t lddk_head, void *dv, int64_t lddv_token, int64_t lddv_head,
+                                        void *workspace, size_t workspace_bytes, void *stream) {
+  nvfp4_status_t st = check_attention_shape(Tq, Tk, Hq, Hkv, D, cu_q, cu_k, B, scale);
+  if (st != NVFP4_OK) return st;
+  if ((Tq == 0 && Tk == 0) || Hq == 0 || B == 0) return NVFP4_OK;
+  const Heads in[] = {{dout, Tq, Hq, lddo_token, lddo_head}, {q, Tq, Hq, ldq_token, ldq_head}, {k, Tk, Hkv, ldk_token, ldk_head},
+                      {v, Tk, Hkv, ldv_token, ldv_head}, {out, Tq, Hq, ldo_token, ldo_head}};
+  const Heads grads[] = {{dq, Tq, Hq, lddq_token, lddq_head}, {dk, Tk, Hkv, lddk_token, lddk_head},
+                         {dv, Tk, Hkv, lddv_token, lddv_head}};
+  for (const Heads &x : in)
+    if ((st = check_heads(x, D, false)) != NVFP4_OK) return st;
+  for (const Heads &x : grads)
+    if ((st = check_heads(x, D, true)) != NVFP4_OK) return st;
+  if (Tq > 0 && !lse) return NVFP4_ERR_NULL;
+  for (const Heads &y : grads)
+    for (const Heads &x : in)
+      if (y.p && y.T > 0 && y.p == x.p) return NVFP4_ERR_STRIDE;
+  if (Tq > 0 && (!workspace || workspace_bytes < nvfp4_attention_backward_workspace_bytes(Tq, Hq)))
+    return NVFP4_ERR_WORKSPACE;
+  if (!aligned(lse, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+  if ((st = check_device()) != NVFP4_OK) return st;
+  const AttentionGradArgs g{{q, k, v, ldq_token, ldq_head, ldk_token, ldk_head, ldv_token, ldv_head, (int)Tq, (int)Tk, (int)Hq,
+                             (int)(Hq / Hkv), (int)D, (int)B, cu_q, cu_k, (int)(Tq / B), (int)(Tk / B), causal != 0, scale,
+                             const_cast<void *>(out), ldo_token, ldo_head, const_cast<float *>(lse)},
+                            dout, lddo_token, lddo_head, dq, dk, dv, lddq_token, lddq_head, lddk_token, lddk_head,
+                            lddv_token, lddv_head, static_cast<float *>(workspace)};
+  return hip_status(launch_attention_backward(g, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"
