@@ -509,6 +509,47 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
                                         int64_t lddk_head, void *dv, int64_t lddv_token, int64_t lddv_head,
                                         void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * A paged cache of keys and values, and the attention of one new token per sequence over it.
+ *
+ *   k_cache, v_cache    [pages][Hkv][page_size][D], 16-byte aligned: bf16, or with k_scales and v_scales the
+ *                       E4M3 codes of MXFP8 (blocks of 32 values along D, the last one of a head shorter
+ *                       where 32 does not divide D).
+ *   k_scales, v_scales  both NULL: a bf16 cache.  Else E8M0 bytes [pages][Hkv][page_size][(D + 31) / 32].
+ *   page_size           a power of two, 16 .. 2^20.   D  8 .. 128, D % 8 == 0.
+ *   page_table          device int32 [B][ld_table], max_pages <= ld_table entries of a row used: position p of
+ *                       sequence b is row p % page_size of page page_table[b][p / page_size].  An entry
+ *                       outside [0, pages) holds no tokens: nothing is read or written there.
+ *   lengths             device int32 [B]: tokens of each sequence, taken into [0, max_pages page_size].
+ *   max_pages page_size < 2^31, B Hkv and B Hq < 2^31, B < 2^16, Hq <= 2^16 with Hq a multiple of Hkv.
+ * No content of page_table, lengths or cu makes a call read or write outside its arrays.
+ *
+ * nvfp4_cache_append writes the keys and values k, v (bf16 [T][Hkv][D] at pitches, as for nvfp4_attention)
+ * of new tokens, which `lengths` counts already: with cu NULL token b is the last one of sequence b
+ * (T == B), else the tokens cu[b] .. cu[b + 1] - 1 are sequence b's last (device int32 [B + 1], ascending).
+ * Tokens past the last sequence, and those whose position is negative or has no page, are not written.  MXFP8 is
+ * bit-identical to nvfp4_mx8_quantize's rule.  Two tokens at one place (a page that two sequences write):
+ * either one's values may remain.  T Hkv (D + 31) / 8 < 2^31.
+ *
+ * nvfp4_paged_attention: out[b] = softmax(scale q[b] . keys) values over the lengths[b] tokens of sequence b
+ * (q, out bf16 [B][Hq][D] at pitches; a sequence without tokens gets 0; out may be q itself with its pitches).  A
+ * sequence's tokens are split over workgroups by its length and joined in a fixed order: equal inputs give
+ * equal bits.  workspace: nvfp4_paged_attention_workspace_bytes bytes (0 where nothing is split; capacity =
+ * max_pages page_size), 16-byte aligned, no initialization.  Nothing past a sequence's length is read.
+ * ------------------------------------------------------------------------------------------- */
+nvfp4_status_t nvfp4_cache_append(const void *k, int64_t ldk_token, int64_t ldk_head, const void *v, int64_t ldv_token,
+                                  int64_t ldv_head, int64_t T, int64_t Hkv, int64_t D, const int32_t *cu,
+                                  const int32_t *lengths, int64_t B, void *k_cache, uint8_t *k_scales, void *v_cache,
+                                  uint8_t *v_scales, int64_t pages, int64_t page_size, const int32_t *page_table,
+                                  int64_t ld_table, int64_t max_pages, void *stream);
+size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity);
+nvfp4_status_t nvfp4_paged_attention(const void *q, int64_t ldq_token, int64_t ldq_head, int64_t B, int64_t Hq,
+                                     int64_t Hkv, int64_t D, const void *k_cache, const uint8_t *k_scales,
+                                     const void *v_cache, const uint8_t *v_scales, int64_t pages, int64_t page_size,
+                                     const int32_t *page_table, int64_t ld_table, int64_t max_pages,
+                                     const int32_t *lengths, float scale, void *out, int64_t ldo_token,
+                                     int64_t ldo_head, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -52,6 +52,7 @@ EXPORTED = (
     "nvfp4_mx8_quantize", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes", "nvfp4_rmsnorm_backward",
     "nvfp4_mx_gemm_w4a8", "nvfp4_rope_axes",
     "nvfp4_attention", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward",
+    "nvfp4_cache_append", "nvfp4_paged_attention_workspace_bytes", "nvfp4_paged_attention",
 )
 
 _lib = None
@@ -152,6 +153,13 @@ def lib():
     L.nvfp4_attention_backward.restype = _i
     L.nvfp4_attention_backward.argtypes = heads * 5 + [_vp] + [_i64] * 5 + [_vp, _vp, _i64, _i, ctypes.c_float] + \
         heads * 3 + [_vp, _sz, _vp]
+    L.nvfp4_cache_append.restype = _i
+    L.nvfp4_cache_append.argtypes = heads * 2 + [_i64] * 3 + [_vp, _vp, _i64] + [_vp] * 4 + [_i64, _i64, _vp, _i64, _i64, _vp]
+    L.nvfp4_paged_attention_workspace_bytes.restype = _sz
+    L.nvfp4_paged_attention_workspace_bytes.argtypes = [_i64] * 5
+    L.nvfp4_paged_attention.restype = _i
+    L.nvfp4_paged_attention.argtypes = heads + [_i64] * 4 + [_vp] * 4 + [_i64, _i64, _vp, _i64, _i64, _vp, ctypes.c_float] + \
+        heads + [_vp, _sz, _vp]
     _lib = L
     return L
 
@@ -954,6 +962,120 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool
     return _Attention.apply(q, k, v, cu_q, cu_k, dict(causal=causal, scale=scale, batch=batch))
 
 
+class PagedCache(NamedTuple):
+    """Keys and values of many sequences in pages: k, v [pages, Hkv, page size, D], bf16, or E4M3 codes (u8) with E8M0
+    scales (u8) [pages, Hkv, page size, ceil(D / 32)]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor | None = None
+    v_scales: torch.Tensor | None = None
+
+
+def paged_cache(pages: int, page_size: int, Hkv: int, D: int, *, mx8: bool = False, device="cuda") -> PagedCache:
+    """A cache's memory (page_size a power of two from 16 on), MXFP8 with mx8; what was never written is never read."""
+    shape = (pages, Hkv, page_size, D)
+    if not mx8:
+        return PagedCache(*(torch.empty(shape, dtype=_bf16, device=device) for _ in range(2)))
+    return PagedCache(*(torch.empty(shape, dtype=_u8, device=device) for _ in range(2)),
+                      *(torch.empty(*shape[:3], (D + 31) // 32, dtype=_u8, device=device) for _ in range(2)))
+
+
+def _paged(cache, page_table, lengths, Hkv: int, D: int, dev: int):
+    """(k, k_scales, v, v_scales addresses, pages, page size, table address, its pitch, pages of a sequence), checked."""
+    k, v, ks, vs = cache
+    if k.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("the cache must be [pages, Hkv, page size, D] and page_table [sequences, pages]")
+    pages, _, size, _ = k.shape
+    shape = (pages, Hkv, size, D)
+    B, most = page_table.shape
+    if (ks is None) != (vs is None):
+        raise ValueError("k_scales and v_scales are given together")
+    dtype, p_ks, p_vs = _bf16, 0, 0
+    if ks is not None:
+        dtype, groups = _u8, (pages, Hkv, size, (D + 31) // 32)
+        p_ks, p_vs = _dense(ks, "k_scales", groups, _u8, dev), _dense(vs, "v_scales", groups, _u8, dev)
+    p_k, p_v = _dense(k, "the cache's k", shape, dtype, dev), _dense(v, "the cache's v", shape, dtype, dev)
+    _dense(lengths, "lengths", (B,), _i32, dev)
+    if page_table.dtype is not _i32 or page_table.get_device() != dev or (page_table.stride(1) != 1 and most > 1):
+        raise ValueError(f"page_table must be int32 with unit stride along pages on cuda:{dev}, got {page_table.dtype} "
+                         f"on {page_table.device}")
+    return p_k, p_ks, p_v, p_vs, pages, size, page_table.data_ptr(), page_table.stride(0) if B > 1 else most, most
+
+
+def nvfp4_cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
+                       lengths: torch.Tensor, cu: torch.Tensor | None = None, *, stream=None) -> None:
+    """Writes the keys and values of new tokens, k, v [T, Hkv, D] bf16 (token and head strides free), into a paged cache.
+
+    lengths int32 [B]: tokens of each sequence, the new ones counted; page_table int32 [B, pages]: where each sequence's
+    pages lie (entries outside the cache: none).  Without cu one token per sequence (T = B); else int32 offsets [B + 1]
+    of each sequence's new tokens, its last ones.  Rounds to MXFP8 where the cache is."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_cache_append(k, v, cache, page_table, lengths, cu)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [T, H, D]")
+    T, Hkv, D = shape = k.shape
+    dev = _launch_device(k)
+    p_k, kt, kh = _heads(k, "k", shape, dev)
+    p_v, vt, vh = _heads(v, "v", shape, dev)
+    ck, cks, cv, cvs, pages, size, table, ld, most = _paged(cache, page_table, lengths, Hkv, D, dev)
+    B = page_table.shape[0]
+    p_cu = 0 if cu is None else _dense(cu, "cu", (B + 1,), _i32, dev)
+    for t in cache:
+        if t is not None:
+            _written(t, "the cache")
+    st = lib().nvfp4_cache_append(p_k, kt, kh, p_v, vt, vh, T, Hkv, D, p_cu, lengths.data_ptr(), B, ck, cks, cv, cvs, pages,
+                                  size, table, ld, most, _current_stream(dev))
+    if st:
+        raise NVFP4Error(st, "nvfp4_cache_append")
+
+
+def nvfp4_paged_attention_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, capacity: int) -> int:
+    return int(lib().nvfp4_paged_attention_workspace_bytes(B, Hq, Hkv, D, capacity))
+
+
+def nvfp4_paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, lengths: torch.Tensor, *,
+                          scale: float | None = None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence, q [B, Hq, D] bf16, over the sequence's tokens in a paged cache (its own
+    key and value appended before).  page_table, lengths as for nvfp4_cache_append; Hq a multiple of the cache's heads.
+    Returns out bf16 [B, Hq, D]; a sequence without tokens gets 0.  scale: D ** -0.5 by default."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nvfp4_paged_attention(q, cache, page_table, lengths, scale=scale, out=out, workspace=workspace)
+    if q.dim() != 3 or cache[0].dim() != 4:
+        raise ValueError("q must be [B, Hq, D] and the cache [pages, Hkv, page size, D]")
+    B, Hq, D = shape = q.shape
+    Hkv = cache[0].shape[1]
+    dev = _launch_device(q)
+    p_q, qt, qh = _heads(q, "q", shape, dev)
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table has {page_table.shape[0]} sequences, q {B}")
+    ck, cks, cv, cvs, pages, size, table, ld, most = _paged(cache, page_table, lengths, Hkv, D, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=_bf16, device=q.device)
+        p_o, ot, oh = out.data_ptr(), Hq * D, D
+    else:
+        p_o, ot, oh = _heads(out, "out", shape, dev)
+        _written(out, "out")
+    L = lib()
+    if workspace is None:
+        n = L.nvfp4_paged_attention_workspace_bytes(B, Hq, Hkv, D, most * size)
+        p_w = 0
+        if n:
+            workspace = torch.empty(n, dtype=_u8, device=q.device)
+            p_w = workspace.data_ptr()
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, not on {q.device}")
+    else:
+        p_w, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = L.nvfp4_paged_attention(p_q, qt, qh, B, Hq, Hkv, D, ck, cks, cv, cvs, pages, size, table, ld, most,
+                                 lengths.data_ptr(), D ** -0.5 if scale is None else scale, p_o, ot, oh, p_w, n,
+                                 _current_stream(dev))
+    if st:
+        raise NVFP4Error(st, "nvfp4_paged_attention")
+    return out
+
+
 __all__ = [
     "Status", "NVFP4Error", "lib", "LIB_PATH", "EXPORTED", "F32", "BF16", "W4A4", "W4A16",
     "SCALE_DYNAMIC", "SCALE_STATIC", "nvfp4_set_debug_checks",
@@ -968,4 +1090,5 @@ __all__ = [
     "nvfp4_rmsnorm_backward", "rmsnorm", "nvfp4_mx_gemm_w4a8",
     "ROPE_PAIRS", "ROPE_HALVES", "rope_inv_freq", "nvfp4_rope_axes", "rope_axes",
     "nvfp4_attention", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward", "attention",
+    "PagedCache", "paged_cache", "nvfp4_cache_append", "nvfp4_paged_attention_workspace_bytes", "nvfp4_paged_attention",
 ]

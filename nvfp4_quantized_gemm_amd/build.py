@@ -11,8 +11,8 @@ BUILD = os.path.join(ROOT, "_build", "nvfp4")
 LIB = os.path.join(PKG, "libnvfp4.so")
 
 SOURCES = ["quantize.hip", "dequantize.hip", "prepack.hip", "gemm.hip", "gemm_skinny.hip", "mxfp4.hip", "rmsnorm.hip",
-           "w4a8.hip", "rope.hip", "attention.hip", "attention_backward.hip", "debug_check.hip", "nvfp4_api.cpp",
-           "nvfp4_mx8_api.cpp", "nvfp4_attention_api.cpp"]
+           "w4a8.hip", "rope.hip", "attention.hip", "attention_backward.hip", "paged_attention.hip",
+           "debug_check.hip", "nvfp4_api.cpp", "nvfp4_mx8_api.cpp", "nvfp4_attention_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = [

@@ -215,4 +215,38 @@ struct AttentionGradArgs {  // attention_backward.hip
 };
 hipError_t launch_attention_backward(const AttentionGradArgs &a, hipStream_t stream);
 
+// A paged cache: [pages][Hkv][page][D] of bf16, or of E4M3 codes with scale bytes [pages][Hkv][page][(D + 31) / 32].
+struct PagedCacheArgs {
+  void *k, *v;
+  uint8_t *ks, *vs;  // null: bf16
+  int pages, page_shift, Hkv, D;
+  const int32_t *table;  // [B][ld_table], of which max_pages entries count
+  int64_t ld_table;
+  int max_pages;
+  const int32_t *lengths;  // [B]
+  int B;
+};
+struct CacheAppendArgs {  // paged_attention.hip
+  PagedCacheArgs c;
+  const void *k, *v;
+  int64_t ldk_t, ldk_h, ldv_t, ldv_h;
+  int T;
+  const int32_t *cu;  // [B + 1], or null: token b is sequence b's
+  FastDiv per_row{}, heads{};  // the launcher sets these
+};
+hipError_t launch_cache_append(CacheAppendArgs a, hipStream_t stream);
+struct PagedAttentionArgs {
+  PagedCacheArgs c;
+  const void *q;
+  int64_t ldq_t, ldq_h;
+  int Hq, group;
+  float scale;
+  void *out;
+  int64_t ldo_t, ldo_h;
+  float *partial;  // workspace: [B][Hq][splits][D], then [B][Hq][splits][2]
+  int splits;
+};
+int paged_attention_splits(int64_t B, int64_t Hq, int64_t Hkv, int64_t capacity);
+hipError_t launch_paged_attention(const PagedAttentionArgs &a, hipStream_t stream);
+
 }  // namespace nvfp4

@@ -45,6 +45,31 @@ nvfp4_status_t check_attention_shape(int64_t Tq, int64_t Tk, int64_t Hq, int64_t
   return NVFP4_OK;
 }
 
+// The shape of a paged cache, and its arrays' extents and alignment.
+nvfp4_status_t check_cache(const void *k, const uint8_t *ks, const void *v, const uint8_t *vs, int64_t pages,
+                           int64_t page_size, const int32_t *table, int64_t ld_table, int64_t max_pages,
+                           const int32_t *lengths, int64_t B, int64_t Hkv, int64_t D) {
+  constexpr int64_t kInt = (int64_t)1 << 31;
+  if (D < 8 || D > kAttentionMaxD || D % 8 != 0 || Hkv < 0 || Hkv > (1 << 16) || B < 0 || B >= (1 << 16) || pages < 0 ||
+      pages >= kInt || page_size < 16 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0 || max_pages < 0 ||
+      max_pages >= kInt / page_size || (Hkv > 0 && pages > kMaxElems / (Hkv * page_size * D)))
+    return NVFP4_ERR_SHAPE;
+  if ((ks == nullptr) != (vs == nullptr)) return NVFP4_ERR_NULL;
+  if (B == 0 || Hkv == 0) return NVFP4_OK;
+  if (!lengths || (max_pages > 0 && !table) || (pages > 0 && (!k || !v))) return NVFP4_ERR_NULL;
+  if (ld_table < max_pages || ld_table > kMaxElems / B) return NVFP4_ERR_STRIDE;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(table, 4) || !aligned(lengths, 4)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+PagedCacheArgs cache_args(const void *k, const uint8_t *ks, const void *v, const uint8_t *vs, int64_t pages,
+                          int64_t page_size, const int32_t *table, int64_t ld_table, int64_t max_pages,
+                          const int32_t *lengths, int64_t B, int64_t Hkv, int64_t D) {
+  int shift = 0;
+  while (((int64_t)1 << shift) < page_size) ++shift;
+  return {const_cast<void *>(k), const_cast<void *>(v), const_cast<uint8_t *>(ks), const_cast<uint8_t *>(vs), (int)pages,
+          shift, (int)Hkv, (int)D, table, ld_table, (int)max_pages, lengths, (int)B};
+}
+
 }  // namespace
 
 extern "C" {
@@ -110,6 +135,72 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
                             dout, lddo_token, lddo_head, dq, dk, dv, lddq_token, lddq_head, lddk_token, lddk_head,
                             lddv_token, lddv_head, static_cast<float *>(workspace)};
   return hip_status(launch_attention_backward(g, static_cast<hipStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_cache_append(const void *k, int64_t ldk_token, int64_t ldk_head, const void *v, int64_t ldv_token,
+                                  int64_t ldv_head, int64_t T, int64_t Hkv, int64_t D, const int32_t *cu,
+                                  const int32_t *lengths, int64_t B, void *k_cache, uint8_t *k_scales, void *v_cache,
+                                  uint8_t *v_scales, int64_t pages, int64_t page_size, const int32_t *page_table,
+                                  int64_t ld_table, int64_t max_pages, void *stream) {
+  constexpr int64_t kThreads = (int64_t)1 << 31;
+  nvfp4_status_t st = check_cache(k_cache, k_scales, v_cache, v_scales, pages, page_size, page_table, ld_table, max_pages,
+                                  lengths, B, Hkv, D);
+  if (st != NVFP4_OK) return st;
+  if (T < 0 || (Hkv > 0 && T >= kThreads / (Hkv * ((D + 31) / 8))) || (!cu && T != B)) return NVFP4_ERR_SHAPE;
+  if (T == 0 || Hkv == 0 || B == 0) return NVFP4_OK;
+  if ((st = check_heads({k, T, Hkv, ldk_token, ldk_head}, D, false)) != NVFP4_OK ||
+      (st = check_heads({v, T, Hkv, ldv_token, ldv_head}, D, false)) != NVFP4_OK)
+    return st;
+  if (!aligned(cu, 4)) return NVFP4_ERR_ALIGN;
+  if ((st = check_device()) != NVFP4_OK) return st;
+  if (pages == 0 || max_pages == 0) return NVFP4_OK;
+  CacheAppendArgs a{};
+  a.c = cache_args(k_cache, k_scales, v_cache, v_scales, pages, page_size, page_table, ld_table, max_pages, lengths, B, Hkv, D);
+  a.k = k;
+  a.v = v;
+  a.ldk_t = ldk_token;
+  a.ldk_h = ldk_head;
+  a.ldv_t = ldv_token;
+  a.ldv_h = ldv_head;
+  a.T = (int)T;
+  a.cu = cu;
+  return hip_status(launch_cache_append(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
+  if (B <= 0 || B >= (1 << 16) || Hq <= 0 || Hq > (1 << 16) || Hkv <= 0 || Hq % Hkv != 0 || D < 8 || D > kAttentionMaxD ||
+      capacity < 0 || capacity >= ((int64_t)1 << 31))
+    return 0;
+  const int splits = paged_attention_splits(B, Hq, Hkv, capacity);
+  return splits > 1 ? sizeof(float) * (size_t)B * (size_t)Hq * (size_t)splits * (size_t)(D + 2) : 0;
+}
+
+nvfp4_status_t nvfp4_paged_attention(const void *q, int64_t ldq_token, int64_t ldq_head, int64_t B, int64_t Hq,
+                                     int64_t Hkv, int64_t D, const void *k_cache, const uint8_t *k_scales,
+                                     const void *v_cache, const uint8_t *v_scales, int64_t pages, int64_t page_size,
+                                     const int32_t *page_table, int64_t ld_table, int64_t max_pages,
+                                     const int32_t *lengths, float scale, void *out, int64_t ldo_token,
+                                     int64_t ldo_head, void *workspace, size_t workspace_bytes, void *stream) {
+  nvfp4_status_t st = check_cache(k_cache, k_scales, v_cache, v_scales, pages, page_size, page_table, ld_table, max_pages,
+                                  lengths, B, Hkv, D);
+  if (st != NVFP4_OK) return st;
+  if (Hq < 0 || Hq > (1 << 16) || (Hq > 0 && (Hkv == 0 || Hq % Hkv != 0))) return NVFP4_ERR_SHAPE;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return NVFP4_ERR_MODE;
+  if (B == 0 || Hq == 0) return NVFP4_OK;
+  const int64_t blocks = Hkv * ((Hq / Hkv + 31) / 32);
+  if (blocks >= (1 << 16)) return NVFP4_ERR_SHAPE;
+  const Heads hq{q, B, Hq, ldq_token, ldq_head}, ho{out, B, Hq, ldo_token, ldo_head};
+  if ((st = check_heads(hq, D, false)) != NVFP4_OK || (st = check_heads(ho, D, true)) != NVFP4_OK) return st;
+  if (!same_place_fits(ho, hq)) return NVFP4_ERR_STRIDE;
+  const size_t need = nvfp4_paged_attention_workspace_bytes(B, Hq, Hkv, D, max_pages * page_size);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+  if ((st = check_device()) != NVFP4_OK) return st;
+  const PagedAttentionArgs a{
+      cache_args(k_cache, k_scales, v_cache, v_scales, pages, page_size, page_table, ld_table, max_pages, lengths, B, Hkv, D),
+      q, ldq_token, ldq_head, (int)Hq, (int)(Hq / Hkv), scale, out, ldo_token, ldo_head, static_cast<float *>(workspace),
+      paged_attention_splits(B, Hq, Hkv, max_pages * page_size)};
+  return hip_status(launch_paged_attention(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
