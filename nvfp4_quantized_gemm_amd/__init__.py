@@ -849,8 +849,8 @@ def _offsets(cu_q, cu_k, batch: int, dev: int):
 def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False, scale: float | None = None,
                     cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, batch: int = 1,
                     save_lse: bool = False, out=None, lse=None, stream=None):
-    """Softmax attention of q [Tq, Hq, D] over k, v [Tk, Hkv, D] (bf16, token and head strides free: views of a QKV
-    output are read in place).  Hq is a multiple of Hkv.  Returns (out, lse): out bf16 [Tq, Hq, D], lse fp32 [Hq, Tq], the
+    """Softmax attention of q [Tq, Hq, D] over k, v [Tk, Hkv, D] (bf16, token strides from D on and head strides free: views
+    of a QKV output are read in place).  Hq is a multiple of Hkv.  Returns (out, lse): out bf16 [Tq, Hq, D], lse fp32 [Hq, Tq], the
     log sums of exponentials that the backward pass reads (None without save_lse or a given lse).
 
     cu_q, cu_k: int32 offsets [sequences + 1] of packed sequences; without them the rows are `batch` sequences of equal
@@ -940,10 +940,17 @@ def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     return tuple(grads)
 
 
+def _token_rows_of(t: torch.Tensor) -> torch.Tensor:
+    """_heads_of, and tokens that overlap (a gradient that autograd has expanded over them) copied too."""
+    t = _heads_of(t)
+    overlap = t.dim() == 3 and t.shape[0] > 1 and t.stride(0) < t.shape[2]
+    return t.clone(memory_format=torch.contiguous_format) if overlap else t
+
+
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_q, cu_k, how):
-        q, k, v = _heads_of(q), _heads_of(k), _heads_of(v)
+        q, k, v = _token_rows_of(q), _token_rows_of(k), _token_rows_of(v)
         out, lse = nvfp4_attention(q, k, v, cu_q=cu_q, cu_k=cu_k, save_lse=True, **how)
         ctx.save_for_backward(q, k, v, out, lse, cu_q, cu_k)
         ctx.how = how
@@ -953,7 +960,7 @@ class _Attention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, cu_q, cu_k = ctx.saved_tensors
-        return *nvfp4_attention_backward(_heads_of(dout), q, k, v, out, lse, cu_q=cu_q, cu_k=cu_k, **ctx.how), None, None, None
+        return *nvfp4_attention_backward(_token_rows_of(dout), q, k, v, out, lse, cu_q=cu_q, cu_k=cu_k, **ctx.how), None, None, None
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False, scale: float | None = None,

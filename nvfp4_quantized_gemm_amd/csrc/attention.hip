@@ -65,80 +65,95 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   auto issue = [&](int t, int buf) {
     uint8_t *at = smem + buf * 2 * kTile;
     const int64_t row = (int64_t)t * kKeys;
-    lk.issue(k + row * a.ldk_t, sk.n - t * kKeys, at, wave);
-    lv.issue(v + row * a.ldv_t, sk.n - t * kKeys, at + kTile, wave);
+    const int left = sk.n - t * kKeys;
+    lk.issue(k + row * a.ldk_t, left, a.ldk_t, a.D, at, wave);
+    lv.issue(v + row * a.ldv_t, left, a.ldv_t, a.D, at + kTile, wave);
   };
 
+  const TileRead<P> read(lane);
   const float scale2 = a.scale * kLog2e;  // exp(scale s) = 2^(scale2 s)
-  float top = -INFINITY, total = 0.0f;    // running maximum of s (both halves of a column), sum (this lane's)
+  float top, total;  // running maximum of s (both halves of a column), sum (this lane's)
   f32x16 O[DB];
-#pragma unroll
-  for (int d = 0; d < DB; ++d) O[d] = zeros16();
 
-  if (tiles > 0) issue(0, 0);
-  for (int t = 0; t < tiles; ++t) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
-    const int key0 = t * kKeys;
-    if (key0 > last_wave) continue;
-    const uint8_t *tk = smem + (t & 1) * 2 * kTile, *tv = tk + kTile;
+  // A pass over the keys; the careful one, which keeps infinities and NaN from queries that do not attend
+  // them, only where a masked tile holds some (as a branch inside one loop it took 40 registers from it).
+  auto pass = [&](const bool careful) __attribute__((always_inline)) {
+    bool again = false;
+    top = -INFINITY;
+    total = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) O[d] = zeros16();
+    if (tiles > 0) issue(0, 0);
+    for (int t = 0; t < tiles; ++t) {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
+      const int key0 = t * kKeys;
+      if (key0 > last_wave) continue;
+      const uint8_t *tk = smem + (t & 1) * 2 * kTile, *tv = tk + kTile;
 
-    f32x16 S[2];
+      f32x16 S[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      S[i] = zeros16();
+      for (int i = 0; i < 2; ++i) {
+        S[i] = zeros16();
 #pragma unroll
-      for (int s = 0; s < KS; ++s) S[i] = mfma(read_rows<P>(tk, 32 * i, s, lane), Q[s], S[i]);
-    }
-    const bool masked = key0 + kKeys - 1 > first_limit;
-    if (masked) {
+        for (int s = 0; s < KS; ++s) S[i] = mfma(read.row_operand(tk, 32 * i, s), Q[s], S[i]);
+      }
+      const bool masked = key0 + kKeys - 1 > first_limit;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) S[i][r] = key0 + 32 * i + c_row(r, h) <= limit ? S[i][r] : -INFINITY;
+      }
+      float m = S[0][0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) m = fmaxf(m, S[0][r]);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) m = fmaxf(m, S[1][r]);
+      m = max_halves(m);
+      // The sums are kept relative to a maximum that may lag by 2^8: they cannot overflow, and are as exact.
+      // Only the queries that need it move theirs, so that a query's bits do not depend on its neighbours.
+      const bool rise = (m - top) * scale2 > 8.0f;
+      if (__ballot(rise)) {
+        const float old = !rise ? 1.0f : top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((top - m) * scale2);
+        top = rise ? m : top;
+        total *= old;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) O[d] *= old;
+      }
+      const float shift = top == -INFINITY ? 0.0f : top * scale2;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[i][r] = key0 + 32 * i + c_row(r, h) <= limit ? S[i][r] : -INFINITY;
-    }
-    float m = S[0][0];
-#pragma unroll
-    for (int r = 1; r < 16; ++r) m = fmaxf(m, S[0][r]);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) m = fmaxf(m, S[1][r]);
-    m = max_halves(m);
-    // The sums are kept relative to a maximum that may lag by 2^8: they cannot overflow, and are as exact.
-    // Only the queries that need it move theirs, so that a query's bits do not depend on its neighbours.
-    const bool rise = (m - top) * scale2 > 8.0f;
-    if (__ballot(rise)) {
-      const float old = !rise ? 1.0f : top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((top - m) * scale2);
-      top = rise ? m : top;
-      total *= old;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) O[d] *= old;
-    }
-    const float shift = top == -INFINITY ? 0.0f : top * scale2;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        S[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i][r], scale2, -shift));
-        total += S[i][r];
-      }
-    const bool apart = masked && tile_nonfinite<P, kKeys>(tv, lane);
-    // rounding the exponentials to bf16 is what the matrix instruction takes: 2^-9 of each, averaged out
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bf16x8 p = as_operand(S[i], s);
-        const int r0 = 32 * i + 16 * s;
-        if (!apart) {
-#pragma unroll
-          for (int d = 0; d < DB; ++d) O[d] = mfma(read_columns<P>(tv, r0, d, lane), p, O[d]);
-        } else {
-          add_rows_apart<P, DB>(tv, r0, p, O, lane, [&](int row) { return key0 + row <= limit; });
+        for (int r = 0; r < 16; ++r) {
+          S[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i][r], scale2, -shift));
+          total += S[i][r];
         }
+      bool apart = masked && tile_nonfinite<P, kKeys>(tv, lane);
+      if (!careful) {
+        again |= apart;
+        apart = false;
       }
-  }
+      // rounding the exponentials to bf16 is what the matrix instruction takes: 2^-9 of each, averaged out
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const bf16x8 p = as_operand(S[i], s);
+          const int r0 = 32 * i + 16 * s;
+          if (!careful || !apart) {
+#pragma unroll
+            for (int d = 0; d < DB; ++d) O[d] = mfma(read.column_operand(tv, r0, d), p, O[d]);
+          } else {
+            add_rows_apart<P, DB>(tv, r0, p, O, read, lane, [&](int row) { return key0 + row <= limit; });
+          }
+        }
+    }
+    return again;
+  };
+  if (__syncthreads_or(pass(false))) pass(true);
 
   total = add_halves(total);
   if (query >= sq.n) return;

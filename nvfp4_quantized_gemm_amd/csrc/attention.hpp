@@ -70,57 +70,74 @@ __device__ __forceinline__ int swizzle(int r) {
   else return (r >> 2) & 3;
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void *base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, 0x7fffffff, 0x00027000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t byte_buffer(const void *base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (int)bytes, 0x00027000);
+}
+// 16 bytes a lane from `bytes` bytes at base to LDS: lane i's to lds + 16 i; zeros past the end.
+__device__ __forceinline__ void buffer_dma16(const void *base, uint32_t bytes, uint8_t *lds, uint32_t lane_off, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(byte_buffer(base, bytes), (lds_void_t *)lds, 16, lane_off, off, 0, 0);
+}
+__device__ __forceinline__ void buffer_dma4(const void *base, uint32_t bytes, uint8_t *lds, uint32_t lane_off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(byte_buffer(base, bytes), (lds_void_t *)lds, 4, lane_off, 0, 0, 0);
 }
 constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer: loads give zeros
 
-// This lane's part of a tile's loads: NI wave-wide 16-byte LDS-DMAs, number j of all (j = wave + NW i) the
-// places 64 j .. 64 j + 63.
+// This lane's part of loading a tile: wave-wide 16-byte LDS-DMAs, number j filling the places 64 j .. 64 j + 63.
+// A wave's DMAs are kN of them, chosen so that what a lane loads repeats (every kPeriod of them, further down).
 template <int P, int ROWS, int NW>
 struct TileLoad {
-  static constexpr int kAll = ROWS * P / 64, kN = (kAll + NW - 1) / NW, kBytes = ROWS * P * 16;
-  uint32_t off[kN];
-  int row[kN];
+  static constexpr int kAll = ROWS * P / 64, kBytes = ROWS * P * 16;
+  static constexpr bool kThree = P == 12;  // 3 DMAs are 16 rows
+  static constexpr int kUnit = kThree ? 3 : 1, kUnits = kAll / kUnit, kN = (kUnits + NW - 1) / NW;
+  static constexpr int kUnitRows = 64 * kUnit / P;
+  static_assert(kUnits * kUnit == kAll && (kThree || P == 4 || NW * kUnitRows % 16 == 0), "the swizzle repeats");
+  uint32_t off[kUnit], step;
   __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int D) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int n = (wave + NW * i) * 64 + lane, r = n / P, p = (n - r * P) ^ swizzle<P>(r);
-      row[i] = r;
+    for (int i = 0; i < kUnit; ++i) {
+      const int n = 64 * i + lane, r = wave * kUnitRows + n / P, p = (n - n / P * P) ^ swizzle<P>(r);
       off[i] = p < D / 8 ? (uint32_t)r * (uint32_t)ld * 2u + 16u * p : kOutside;
     }
+    step = NW * kUnitRows * (uint32_t)ld * 2u;
   }
-  // rows past `left` and pieces past D become zeros
-  __device__ __forceinline__ void issue(const uint16_t *base, int left, uint8_t *lds, int wave) const {
-    const __amdgpu_buffer_rsrc_t rsrc = row_buffer(base);
+  // The first `left` rows from base on; what lies past their last value is loaded as zeros (pitch >= D).
+  __device__ __forceinline__ void issue(const uint16_t *base, int left, int64_t ld, int D, uint8_t *lds, int wave) const {
+    const uint32_t bytes = left > 0 ? (uint32_t)(min(left, ROWS) - 1) * (uint32_t)ld * 2u + 2u * D : 0u;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int j = wave + NW * i;
-      if (kAll % NW != 0 && j >= kAll) break;
-      const uint32_t o = row[i] < left ? off[i] : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t *)(lds + 1024 * j), 16, o, 0, 0, 0);
+    for (int u = 0; u < kN; ++u) {
+      if (kUnits % NW != 0 && wave + NW * u >= kUnits) break;
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i)
+        buffer_dma16(base, bytes, lds + 1024 * (kUnit * (wave + NW * u) + i), off[i], u * step);
     }
   }
 };
 
-// A operand, rows r0 .. r0 + 31, values 16 s .. 16 s + 15 of a tile.
+// Where this lane reads a tile, so that the places of other steps, blocks and rows are an exclusive or with a
+// constant and the instruction's offset.
 template <int P>
-__device__ __forceinline__ bf16x8 read_rows(const uint8_t *tile, int r0, int s, int lane) {
-  const int r = r0 + (lane & 31);
-  return *reinterpret_cast<const bf16x8 *>(tile + r * (P * 16) + (((2 * s + (lane >> 5)) ^ swizzle<P>(r)) << 4));
-}
-// A operand of the transposed tile: rows are values 32 d .. 32 d + 31, k rows r0 + kappa(0, h, 0 .. 7) (r0 a
-// multiple of 16).  Each of the two reads turns 4 rows of 16 values per 16 lanes.
-template <int P>
-__device__ __forceinline__ bf16x8 read_columns(const uint8_t *tile, int r0, int d, int lane) {
-  const int i = lane & 15, r = r0 + 4 * (lane >> 5) + (i >> 2);
-  const int p = 4 * d + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
-  const uint8_t *at = tile + 8 * (i & 1);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + r * (P * 16) + ((p ^ swizzle<P>(r)) << 4)));
-  const s16x4 b =
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + (r + 8) * (P * 16) + ((p ^ swizzle<P>(r + 8)) << 4)));
-  return __builtin_bit_cast(bf16x8, s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
-}
+struct TileRead {
+  static constexpr bool kXor = P == 8 || P == 16;
+  uint32_t rows, columns;
+  __device__ __forceinline__ explicit TileRead(int lane) {
+    const int r = lane & 31, h = lane >> 5, i = lane & 15, k = 4 * h + (i >> 2);
+    rows = r * (P * 16) + ((h ^ swizzle<P>(r)) << 4);
+    columns = k * (P * 16) + (((2 * ((lane >> 4) & 1) + ((i >> 1) & 1)) ^ swizzle<P>(k)) << 4) + 8 * (i & 1);
+  }
+  // A operand: rows r0 .. r0 + 31 (r0 a multiple of 16), values 16 s .. 16 s + 15.
+  __device__ __forceinline__ bf16x8 row_operand(const uint8_t *tile, int r0, int s) const {
+    const uint32_t at = kXor ? rows ^ (s << 5) : (rows ^ ((s & 1) << 5)) + ((s >> 1) << 6);
+    return *reinterpret_cast<const bf16x8 *>(tile + at + r0 * (P * 16));
+  }
+  // A operand of the transposed tile: rows are values 32 d .. 32 d + 31, k rows r0 + kappa(0, h, 0 .. 7) (r0 a
+  // multiple of 16).  Each of the two reads turns 4 rows of 16 values per 16 lanes.
+  __device__ __forceinline__ bf16x8 column_operand(const uint8_t *tile, int r0, int d) const {
+    const uint32_t at = kXor ? columns ^ (d << 6) : columns + (d << 6);
+    const uint8_t *p = tile + at + r0 * (P * 16), *q = tile + (at ^ 32) + (r0 + 8) * (P * 16);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p), b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)q);
+    return __builtin_bit_cast(bf16x8, s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+  }
+};
 
 // B operand from global memory: column c is row c of [n][ld], zeros past row n - 1 and past D.
 __device__ __forceinline__ bf16x8 load_column_operand(const uint16_t *base, int64_t ld, int row, int n, int s, int D,
@@ -189,15 +206,15 @@ __device__ __forceinline__ bool tile_nonfinite(const uint8_t *tile, int lane) {
 // are multiplied as always, so what no other value touches has the same bits; then the others, each row
 // alone, added only to the columns that see it.  sees(row): whether this lane's column does.
 template <int P, int DB, typename Sees>
-__device__ __forceinline__ void add_rows_apart(const uint8_t *tile, int r0, const bf16x8 &b, f32x16 (&c)[DB], int lane,
-                                               Sees sees) {
+__device__ __forceinline__ void add_rows_apart(const uint8_t *tile, int r0, const bf16x8 &b, f32x16 (&c)[DB],
+                                               const TileRead<P> &at, int lane, Sees sees) {
   auto split = [](uint32_t w, bool finite) {  // the halves of w that are finite, or those that are not
     const uint32_t bad = ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
     return finite ? w & ~bad : w & bad;
   };
 #pragma unroll
   for (int d = 0; d < DB; ++d) {
-    u32x4 w = __builtin_bit_cast(u32x4, read_columns<P>(tile, r0, d, lane));
+    u32x4 w = __builtin_bit_cast(u32x4, at.column_operand(tile, r0, d));
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = split(w[i], true);
     c[d] = mfma(__builtin_bit_cast(bf16x8, w), b, c[d]);
@@ -208,7 +225,7 @@ __device__ __forceinline__ void add_rows_apart(const uint8_t *tile, int r0, cons
     const bool add = sees(r0 + row);
 #pragma unroll
     for (int d = 0; d < DB; ++d) {
-      u32x4 w = __builtin_bit_cast(u32x4, read_columns<P>(tile, r0, d, lane));
+      u32x4 w = __builtin_bit_cast(u32x4, at.column_operand(tile, r0, d));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         w[i] = (lane >> 5) == h && e >> 1 == i ? split(w[i], false) & (e & 1 ? 0xffff0000u : 0xffffu) : 0u;

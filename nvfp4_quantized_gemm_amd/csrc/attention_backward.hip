@@ -82,51 +82,62 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   auto issue = [&](int t, int buf) {
     uint8_t *to = smem + buf * 2 * kTile;
     const int64_t row = (int64_t)t * kRows;
-    lk.issue(k + row * a.ldk_t, sk.n - t * kRows, to, wave);
-    lv.issue(v + row * a.ldv_t, sk.n - t * kRows, to + kTile, wave);
+    const int left = sk.n - t * kRows;
+    lk.issue(k + row * a.ldk_t, left, a.ldk_t, a.D, to, wave);
+    lv.issue(v + row * a.ldv_t, left, a.ldv_t, a.D, to + kTile, wave);
   };
+  const TileRead<P> read(lane);
   const float scale2 = a.scale * kLog2e;
   f32x16 dQ[DB];
-#pragma unroll
-  for (int d = 0; d < DB; ++d) dQ[d] = zeros16();
 
-  if (tiles > 0) issue(0, 0);
-  for (int t = 0; t < tiles; ++t) {
-    tile_barrier();
-    if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
-    const int key0 = t * kRows;
-    if (key0 > last_wave) continue;
-    const uint8_t *tk = smem + (t & 1) * 2 * kTile, *tv = tk + kTile;
-    const bool masked = key0 + kRows - 1 > first_limit;
-    const bool apart = masked && tile_nonfinite<P, kRows>(tk, lane);
+  auto pass = [&](const bool careful) __attribute__((always_inline)) {  // see k_attention
+    bool again = false;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f32x16 S = zeros16(), dP = zeros16();
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        S = mfma(read_rows<P>(tk, 32 * i, s, lane), Q[s], S);
-        dP = mfma(read_rows<P>(tv, 32 * i, s, lane), dO[s], dP);
+    for (int d = 0; d < DB; ++d) dQ[d] = zeros16();
+    if (tiles > 0) issue(0, 0);
+    for (int t = 0; t < tiles; ++t) {
+      tile_barrier();
+      if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
+      const int key0 = t * kRows;
+      if (key0 > last_wave) continue;
+      const uint8_t *tk = smem + (t & 1) * 2 * kTile, *tv = tk + kTile;
+      const bool masked = key0 + kRows - 1 > first_limit;
+      bool apart = masked && tile_nonfinite<P, kRows>(tk, lane);
+      if (!careful) {
+        again |= apart;
+        apart = false;
       }
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        S[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], scale2, -lse2)) * (dP[r] - delta);
-      if (masked) {
+      for (int i = 0; i < 2; ++i) {
+        f32x16 S = zeros16(), dP = zeros16();
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[r] = key0 + 32 * i + c_row(r, h) <= limit ? S[r] : 0.0f;
-      }
+        for (int s = 0; s < KS; ++s) {
+          S = mfma(read.row_operand(tk, 32 * i, s), Q[s], S);
+          dP = mfma(read.row_operand(tv, 32 * i, s), dO[s], dP);
+        }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bf16x8 ds = as_operand(S, s);
-        const int r0 = 32 * i + 16 * s;
-        if (!apart) {
+        for (int r = 0; r < 16; ++r)
+          S[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[r], scale2, -lse2)) * (dP[r] - delta);
+        if (masked) {
 #pragma unroll
-          for (int d = 0; d < DB; ++d) dQ[d] = mfma(read_columns<P>(tk, r0, d, lane), ds, dQ[d]);
-        } else {
-          add_rows_apart<P, DB>(tk, r0, ds, dQ, lane, [&](int row) { return key0 + row <= limit; });
+          for (int r = 0; r < 16; ++r) S[r] = key0 + 32 * i + c_row(r, h) <= limit ? S[r] : 0.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const bf16x8 ds = as_operand(S, s);
+          const int r0 = 32 * i + 16 * s;
+          if (!careful || !apart) {
+#pragma unroll
+            for (int d = 0; d < DB; ++d) dQ[d] = mfma(read.column_operand(tk, r0, d), ds, dQ[d]);
+          } else {
+            add_rows_apart<P, DB>(tk, r0, ds, dQ, read, lane, [&](int row) { return key0 + row <= limit; });
+          }
         }
       }
     }
-  }
+    return again;
+  };
+  if (__syncthreads_or(pass(false))) pass(true);
   if (query >= sq.n) return;
   store_column<DB>(dQ, a.scale, static_cast<uint16_t *>(g.dq) + (int64_t)(sq.begin + query) * g.lddq_t + head * g.lddq_h, a.D, h);
 }
@@ -162,85 +173,95 @@ __global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(RS
   TileLoad<P, kRows, NW> lq, lo;
   lq.init(wave, lane, a.ldq_t, a.D);
   lo.init(wave, lane, g.lddo_t, a.D);
-  int ih = 0, it = first_tile;  // the next step to load: head of the group, tile
+  int ih, it;  // the next step to load: head of the group, tile
   auto issue = [&](int buf) {
     uint8_t *to = smem + buf * kStage;
     const int head = kv * a.group + ih;
     const int64_t row = sq.begin + (int64_t)it * kRows;
-    const int left = sq.n - it * kRows;
-    lq.issue(static_cast<const uint16_t *>(a.q) + row * a.ldq_t + head * a.ldq_h, left, to, wave);
-    lo.issue(static_cast<const uint16_t *>(g.dout) + row * g.lddo_t + head * g.lddo_h, left, to + kTile, wave);
+    const int left = min(sq.n - it * kRows, kRows);
+    lq.issue(static_cast<const uint16_t *>(a.q) + row * a.ldq_t + head * a.ldq_h, left, a.ldq_t, a.D, to, wave);
+    lo.issue(static_cast<const uint16_t *>(g.dout) + row * g.lddo_t + head * g.lddo_h, left, g.lddo_t, a.D, to + kTile, wave);
     if (wave < 2) {  // the rows' log sums, and their sums of dO O
       const float *rows = g.rows + ((int64_t)wave * a.Hq + head) * a.Tq + row;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(rows), (lds_void_t *)(to + 2 * kTile + wave * kRows * 4), 4,
-                                               lane < left ? 4 * lane : kOutside, 0, 0, 0);
+      buffer_dma4(rows, left > 0 ? 4 * min(left, kRows) : 0, to + 2 * kTile + wave * kRows * 4, 4 * lane);
     }
     if (++it == tiles) {
       it = first_tile;
       ++ih;
     }
   };
+  const TileRead<P> read(lane);
   const float scale2 = a.scale * kLog2e;
   f32x16 dK[DB], dV[DB];
+  auto pass = [&](const bool careful) __attribute__((always_inline)) {  // see k_attention
+    bool again = false;
+    ih = 0;
+    it = first_tile;
 #pragma unroll
-  for (int d = 0; d < DB; ++d) dK[d] = dV[d] = zeros16();
-
-  if (steps > 0) issue(0);
-  int t = first_tile;
-  for (int step = 0; step < steps; ++step) {
-    tile_barrier();
-    if (step + 1 < steps) issue((step + 1) & 1);
-    const uint8_t *tq = smem + (step & 1) * kStage, *to = tq + kTile;
-    const float *rows = reinterpret_cast<const float *>(tq + 2 * kTile);
-    const int tile0 = t * kRows;
-    t = t + 1 == tiles ? first_tile : t + 1;
-    const bool masked = tile0 < last_first;
-    if (tile0 + kRows - 1 < first_wave) continue;
-    const bool apart = masked && (tile_nonfinite<P, kRows>(tq, lane) || tile_nonfinite<P, kRows>(to, lane));
-#pragma unroll
-    for (int j = 0; j < 2 / RS; ++j) {
-      const int i = RS == 2 ? rs : j, row0 = tile0 + 32 * i;
-      f32x16 S = zeros16(), dP = zeros16();
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        S = mfma(read_rows<P>(tq, 32 * i, s, lane), K[s], S);
-        dP = mfma(read_rows<P>(to, 32 * i, s, lane), V[s], dP);
+    for (int d = 0; d < DB; ++d) dK[d] = dV[d] = zeros16();
+    if (steps > 0) issue(0);
+    int t = first_tile;
+    for (int step = 0; step < steps; ++step) {
+      tile_barrier();
+      if (step + 1 < steps) issue((step + 1) & 1);
+      const uint8_t *tq = smem + (step & 1) * kStage, *to = tq + kTile;
+      const float *rows = reinterpret_cast<const float *>(tq + 2 * kTile);
+      const int tile0 = t * kRows;
+      t = t + 1 == tiles ? first_tile : t + 1;
+      const bool masked = tile0 < last_first;
+      if (tile0 + kRows - 1 < first_wave) continue;
+      bool apart = masked && (tile_nonfinite<P, kRows>(tq, lane) || tile_nonfinite<P, kRows>(to, lane));
+      if (!careful) {
+        again |= apart;
+        apart = false;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(rows + 32 * i + 8 * u + 4 * h);
-        const f32x4 delta = *reinterpret_cast<const f32x4 *>(rows + kRows + 32 * i + 8 * u + 4 * h);
+      for (int j = 0; j < 2 / RS; ++j) {
+        const int i = RS == 2 ? rs : j, row0 = tile0 + 32 * i;
+        f32x16 S = zeros16(), dP = zeros16();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          S[4 * u + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * u + e], scale2, -lse2[e]));
-          dP[4 * u + e] = S[4 * u + e] * (dP[4 * u + e] - delta[e]);
+        for (int s = 0; s < KS; ++s) {
+          S = mfma(read.row_operand(tq, 32 * i, s), K[s], S);
+          dP = mfma(read.row_operand(to, 32 * i, s), V[s], dP);
         }
-      }
-      if (masked) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const bool in = row0 + c_row(r, h) >= first_row;
-          S[r] = in ? S[r] : 0.0f;
-          dP[r] = in ? dP[r] : 0.0f;
-        }
-      }
+        for (int u = 0; u < 4; ++u) {
+          const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(rows + 32 * i + 8 * u + 4 * h);
+          const f32x4 delta = *reinterpret_cast<const f32x4 *>(rows + kRows + 32 * i + 8 * u + 4 * h);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bf16x8 p = as_operand(S, s), ds = as_operand(dP, s);
-        const int r0 = 32 * i + 16 * s;
-        if (!apart) {
-#pragma unroll
-          for (int d = 0; d < DB; ++d) {
-            dV[d] = mfma(read_columns<P>(to, r0, d, lane), p, dV[d]);
-            dK[d] = mfma(read_columns<P>(tq, r0, d, lane), ds, dK[d]);
+          for (int e = 0; e < 4; ++e) {
+            S[4 * u + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * u + e], scale2, -lse2[e]));
+            dP[4 * u + e] = S[4 * u + e] * (dP[4 * u + e] - delta[e]);
           }
-        } else {
-          add_rows_apart<P, DB>(to, r0, p, dV, lane, [&](int row) { return tile0 + row >= first_row; });
-          add_rows_apart<P, DB>(tq, r0, ds, dK, lane, [&](int row) { return tile0 + row >= first_row; });
+        }
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const bool in = row0 + c_row(r, h) >= first_row;
+            S[r] = in ? S[r] : 0.0f;
+            dP[r] = in ? dP[r] : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const bf16x8 p = as_operand(S, s), ds = as_operand(dP, s);
+          const int r0 = 32 * i + 16 * s;
+          if (!careful || !apart) {
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              dV[d] = mfma(read.column_operand(to, r0, d), p, dV[d]);
+              dK[d] = mfma(read.column_operand(tq, r0, d), ds, dK[d]);
+            }
+          } else {
+            add_rows_apart<P, DB>(to, r0, p, dV, read, lane, [&](int row) { return tile0 + row >= first_row; });
+            add_rows_apart<P, DB>(tq, r0, ds, dK, read, lane, [&](int row) { return tile0 + row >= first_row; });
+          }
         }
       }
     }
-  }
+    return again;
+  };
+  if (__syncthreads_or(pass(false))) pass(true);
   if constexpr (RS == 2) {  // the second half's sums join the first's
     f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + kw * (DB * 4 * 64) + lane;
     auto join = [&](f32x16(&x)[DB]) {

@@ -21,10 +21,12 @@ struct Heads {  // [T][H][D] bf16 at token and head pitches
 nvfp4_status_t check_heads(const Heads &x, int64_t D, bool written) {
   if (x.T == 0 || x.H == 0) return NVFP4_OK;
   if (!x.p) return NVFP4_ERR_NULL;
-  if (x.ld_t >= kMaxPitch || !head_rows_fit(x.T, x.H, D, x.ld_t, x.ld_h, written)) return NVFP4_ERR_STRIDE;
+  if ((x.T > 1 && x.ld_t < D) || x.ld_t >= kMaxPitch || !head_rows_fit(x.T, x.H, D, x.ld_t, x.ld_h, written)) return NVFP4_ERR_STRIDE;
   if (!rows_aligned(x.p, x.ld_t, NVFP4_BF16) || !rows_aligned(x.p, x.ld_h, NVFP4_BF16)) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
 }
+// the token pitch that the kernels bound their rows by; a single token's is never used, whatever it is
+int64_t row_pitch(const Heads &x, int64_t D) { return x.T > 1 ? x.ld_t : D; }
 // a written array at an input's address has its pitches
 bool same_place_fits(const Heads &out, const Heads &in) {
   return out.p != in.p || ((out.T <= 1 || out.ld_t == in.ld_t) && (out.H <= 1 || out.ld_h == in.ld_h));
@@ -90,7 +92,7 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
   if (!same_place_fits(ho, hq)) return NVFP4_ERR_STRIDE;
   if (!aligned(lse, 4)) return NVFP4_ERR_ALIGN;
   if ((st = check_device()) != NVFP4_OK) return st;
-  const AttentionArgs a{q, k, v, ldq_token, ldq_head, ldk_token, ldk_head, ldv_token, ldv_head, (int)Tq, (int)Tk, (int)Hq,
+  const AttentionArgs a{q, k, v, row_pitch(hq, D), ldq_head, row_pitch(hk, D), ldk_head, row_pitch(hv, D), ldv_head, (int)Tq, (int)Tk, (int)Hq,
                         (int)(Hq / Hkv), (int)D, (int)B, cu_q, cu_k, (int)(Tq / B), (int)(Tk / B), causal != 0, scale, out,
                         ldo_token, ldo_head, lse};
   return hip_status(launch_attention(a, static_cast<hipStream_t>(stream)));
@@ -129,10 +131,10 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
     return NVFP4_ERR_WORKSPACE;
   if (!aligned(lse, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
   if ((st = check_device()) != NVFP4_OK) return st;
-  const AttentionGradArgs g{{q, k, v, ldq_token, ldq_head, ldk_token, ldk_head, ldv_token, ldv_head, (int)Tq, (int)Tk, (int)Hq,
+  const AttentionGradArgs g{{q, k, v, row_pitch(in[1], D), ldq_head, row_pitch(in[2], D), ldk_head, row_pitch(in[3], D), ldv_head, (int)Tq, (int)Tk, (int)Hq,
                              (int)(Hq / Hkv), (int)D, (int)B, cu_q, cu_k, (int)(Tq / B), (int)(Tk / B), causal != 0, scale,
                              const_cast<void *>(out), ldo_token, ldo_head, const_cast<float *>(lse)},
-                            dout, lddo_token, lddo_head, dq, dk, dv, lddq_token, lddq_head, lddk_token, lddk_head,
+                            dout, row_pitch(in[0], D), lddo_head, dq, dk, dv, lddq_token, lddq_head, lddk_token, lddk_head,
                             lddv_token, lddv_head, static_cast<float *>(workspace)};
   return hip_status(launch_attention_backward(g, static_cast<hipStream_t>(stream)));
 }

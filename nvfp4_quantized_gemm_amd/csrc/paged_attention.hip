@@ -128,8 +128,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
       next_ok[half] = page >= 0 && page < c.pages;
       const int64_t at = next_ok[half] ? (((int64_t)page * c.Hkv + kv) << c.page_shift) + (pos & mask) : 0;
       const int left = next_ok[half] ? hi - pos : 0;
-      const __amdgpu_buffer_rsrc_t bk = row_buffer(static_cast<const uint8_t *>(c.k) + at * c.D * ES),
-                                   bv = row_buffer(static_cast<const uint8_t *>(c.v) + at * c.D * ES);
+      const __amdgpu_buffer_rsrc_t bk = byte_buffer(static_cast<const uint8_t *>(c.k) + at * c.D * ES, 0x7fffffffu),
+                                   bv = byte_buffer(static_cast<const uint8_t *>(c.v) + at * c.D * ES, 0x7fffffffu);
 #pragma unroll
       for (int i = half * kN / 2; i < (half + 1) * kN / 2; ++i) {
         const uint32_t o = (row[i] & 15) < left ? off[i] : kOutside;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
         }
       }
       if constexpr (MX8) {
-        const __amdgpu_buffer_rsrc_t sk = row_buffer(c.ks + at * nb), sv = row_buffer(c.vs + at * nb);
+        const __amdgpu_buffer_rsrc_t sk = byte_buffer(c.ks + at * nb, 0x7fffffffu), sv = byte_buffer(c.vs + at * nb, 0x7fffffffu);
 #pragma unroll
         for (int i = half * kN / 2; i < (half + 1) * kN / 2; ++i) {
           const uint32_t o = (row[i] & 15) < left ? soff[i] : kOutside;
@@ -163,6 +163,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     ok[1] = next_ok[1];
   };
 
+  const TileRead<P> read(lane);
   const float scale2 = a.scale * kLog2e;
   float top = -INFINITY, total = 0.0f;
   f32x16 O[DB];
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     f32x16 S = zeros16();
 #pragma unroll
-    for (int s = 0; s < KS; ++s) S = mfma(read_rows<P>(tk, 0, s, lane), Q[s], S);
+    for (int s = 0; s < KS; ++s) S = mfma(read.row_operand(tk, 0, s), Q[s], S);
     if (key0 + kTileKeys > hi || !ok[0] || !ok[1]) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) S[r] = key0 + c_row(r, h) < hi && ok[r >> 3] ? S[r] : -INFINITY;
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     for (int s = 0; s < 2; ++s) {
       const bf16x8 p = as_operand(S, s);
 #pragma unroll
-      for (int d = 0; d < DB; ++d) O[d] = mfma(read_columns<P>(tv, 16 * s, d, lane), p, O[d]);
+      for (int d = 0; d < DB; ++d) O[d] = mfma(read.column_operand(tv, 16 * s, d), p, O[d]);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }

@@ -147,8 +147,8 @@ def test_views_of_a_qkv_output_and_other_pitches():
     assert got[0] is out and torch.equal(out, want[0])
     same = q.clone()
     assert torch.equal(nv.nvfp4_attention(same, k, v, causal=True, out=same)[0], want[0]) and torch.equal(same, want[0])
-    # one key and one value for all tokens and heads
-    k1, v1 = k[:1, :1].expand(T, H, D), v[:1, :1].expand(T, H, D)
+    # one key and one value head in the place of all
+    k1, v1 = k[:, :1].expand(T, H, D), v[:, :1].expand(T, H, D)
     a = nv.nvfp4_attention(q, k1, v1)[0]
     assert torch.equal(a, nv.nvfp4_attention(q, k1.contiguous(), v1.contiguous())[0])
 
