@@ -496,9 +496,11 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
  *   dout, out, dq   bf16 [Tq][Hq][D], dk, dv bf16 [Tk][Hkv][D], at their own pitches as above.
  *   dq, dk, dv      written; at no input's address (NVFP4_ERR_STRIDE) and not overlapping any array.  Rows
  *                   past the last sequence are left as they were; keys that nothing attends get 0.
- *   workspace       nvfp4_attention_backward_workspace_bytes(Tq, Hq) bytes, 16-byte aligned, no initialization.
+ *   workspace       nvfp4_attention_backward_workspace_bytes bytes, 16-byte aligned, no initialization (where there
+ *                   are few keys, several workgroups share their gradients and add them at the end).
  * B == 0 or Hq == 0 is valid and touches nothing; Tq == 0 writes dk = dv = 0. */
-size_t nvfp4_attention_backward_workspace_bytes(int64_t Tq, int64_t Hq);
+size_t nvfp4_attention_backward_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
+                                                int64_t B);
 nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, int64_t lddo_head, const void *q,
                                         int64_t ldq_token, int64_t ldq_head, const void *k, int64_t ldk_token,
                                         int64_t ldk_head, const void *v, int64_t ldv_token, int64_t ldv_head,

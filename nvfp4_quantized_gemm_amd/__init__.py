@@ -149,7 +149,7 @@ def lib():
     L.nvfp4_attention.restype = _i
     L.nvfp4_attention.argtypes = heads * 3 + [_i64] * 5 + [_vp, _vp, _i64, _i, ctypes.c_float] + heads + [_vp, _vp]
     L.nvfp4_attention_backward_workspace_bytes.restype = _sz
-    L.nvfp4_attention_backward_workspace_bytes.argtypes = [_i64, _i64]
+    L.nvfp4_attention_backward_workspace_bytes.argtypes = [_i64] * 6
     L.nvfp4_attention_backward.restype = _i
     L.nvfp4_attention_backward.argtypes = heads * 5 + [_vp] + [_i64] * 5 + [_vp, _vp, _i64, _i, ctypes.c_float] + \
         heads * 3 + [_vp, _sz, _vp]
@@ -891,8 +891,8 @@ def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal
     return out, lse
 
 
-def nvfp4_attention_backward_workspace_bytes(Tq: int, Hq: int) -> int:
-    return int(lib().nvfp4_attention_backward_workspace_bytes(Tq, Hq))
+def nvfp4_attention_backward_workspace_bytes(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, batch: int) -> int:
+    return int(lib().nvfp4_attention_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch))
 
 
 def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -925,7 +925,7 @@ def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
         grads.append(t)
     L = lib()
     if workspace is None:
-        n = L.nvfp4_attention_backward_workspace_bytes(Tq, Hq)
+        n = L.nvfp4_attention_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch)
         workspace = torch.empty(n, dtype=_u8, device=q.device)
     elif workspace.get_device() != dev:
         raise ValueError(f"workspace is on {workspace.device}, not on {q.device}")

@@ -178,6 +178,18 @@ __device__ __forceinline__ void store_column(const f32x16 (&c)[DB], float f, uin
     }
 }
 
+template <int DB>
+__device__ __forceinline__ void store_column_f32(const f32x16 (&c)[DB], float f, float *out, int D, int h) {
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int at = 32 * d + 8 * g + 4 * h;
+      if (at >= D) continue;
+      *reinterpret_cast<f32x4 *>(out + at) = f32x4{c[d][4 * g] * f, c[d][4 * g + 1] * f, c[d][4 * g + 2] * f, c[d][4 * g + 3] * f};
+    }
+}
+
 // Over the two lanes that share a column.
 __device__ __forceinline__ float max_halves(float v) {
   const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);

@@ -142,33 +142,44 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   store_column<DB>(dQ, a.scale, static_cast<uint16_t *>(g.dq) + (int64_t)(sq.begin + query) * g.lddq_t + head * g.lddq_h, a.D, h);
 }
 
-// KW waves of 32 keys; RS waves take turns at the 32-row halves of a tile, and their sums are added at the end.
-template <int KS, int DB, int KW, int RS>
-__global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(RS, RS))) void k_attention_dkv(const AttentionGradArgs g) {
+// KW waves of 32 keys; the two waves of a block of keys take a tile's 32-row halves, and their sums are added at the
+// end.  The steps (query heads of the group, times their tiles) of a block of keys are shared by a.splits workgroups,
+// whose sums a second kernel adds.  VL: the value operands are read from LDS at every use (with 128 values a head
+// they would be registers too many for two waves per SIMD).
+template <int KS, int DB, int KW, bool VL>
+__global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attention_dkv(const AttentionGradArgs g) {
   const AttentionArgs &a = g.f;
-  constexpr int P = 4 * DB, BK = 32 * KW, NW = KW * RS, kTile = kRows * P * 16, kStage = 2 * kTile + 2 * kRows * 4;
+  constexpr int P = 4 * DB, BK = 32 * KW, NW = 2 * KW, kTile = kRows * P * 16, kStage = 2 * kTile + 2 * kRows * 4;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  uint8_t *const tv = smem + 2 * kStage;  // VL: the block's values
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kw = wave % KW, rs = wave / KW;
   int kv, slot, b, blk;
-  block_of(a.Hq / a.group, a.slots, a.causal, kv, slot);
-  find_block<BK>(slot, a.cu_k, a.B, a.Tk, a.per_k, lane, b, blk);
+  block_of(a.Hq / a.group, a.slots * g.splits, a.causal, kv, slot);
+  const int split = slot % g.splits;
+  find_block<BK>(slot / g.splits, a.cu_k, a.B, a.Tk, a.per_k, lane, b, blk);
   const SeqRows sq = seq_rows(a.cu_q, b, a.Tq, a.per_q), sk = seq_rows(a.cu_k, b, a.Tk, a.per_k);
   if (blk < 0 || blk * BK >= sk.n) return;
   const int k0 = blk * BK + 32 * kw, key = k0 + c, ahead = sk.n - sq.n;
   const uint16_t *k = static_cast<const uint16_t *>(a.k) + sk.begin * a.ldk_t + kv * a.ldk_h;
   const uint16_t *v = static_cast<const uint16_t *>(a.v) + sk.begin * a.ldv_t + kv * a.ldv_h;
-  bf16x8 K[KS], V[KS];
+  bf16x8 K[KS], V[VL ? 1 : KS];
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     K[s] = load_column_operand(k, a.ldk_t, key, sk.n, s, a.D, lane);
-    V[s] = load_column_operand(v, a.ldv_t, key, sk.n, s, a.D, lane);
+    if constexpr (!VL) V[s] = load_column_operand(v, a.ldv_t, key, sk.n, s, a.D, lane);
+  }
+  if constexpr (VL) {  // the first step's barrier waits for it
+    TileLoad<P, BK, NW> lv;
+    lv.init(wave, lane, a.ldv_t, a.D);
+    lv.issue(v + (int64_t)blk * BK * a.ldv_t, sk.n - blk * BK, a.ldv_t, a.D, tv, wave);
   }
   // the first query that attends a key j is j - ahead
   const int first_row = a.causal ? key - ahead : 0;
   const int last_first = a.causal ? k0 + 31 - ahead : 0, first_wave = a.causal ? max(k0 - ahead, 0) : 0;
   const int first_tile = (a.causal ? max(blk * BK - ahead, 0) : 0) / kRows, tiles = (sq.n + kRows - 1) / kRows;
-  const int steps = tiles > first_tile ? (tiles - first_tile) * a.group : 0;
+  const int per_head = max(tiles - first_tile, 0), steps = per_head * a.group;
+  const int begin = (int)((int64_t)steps * split / g.splits), end = (int)((int64_t)steps * (split + 1) / g.splits);
 
   TileLoad<P, kRows, NW> lq, lo;
   lq.init(wave, lane, a.ldq_t, a.D);
@@ -178,7 +189,7 @@ __global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(RS
     uint8_t *to = smem + buf * kStage;
     const int head = kv * a.group + ih;
     const int64_t row = sq.begin + (int64_t)it * kRows;
-    const int left = min(sq.n - it * kRows, kRows);
+    const int left = sq.n - it * kRows;
     lq.issue(static_cast<const uint16_t *>(a.q) + row * a.ldq_t + head * a.ldq_h, left, a.ldq_t, a.D, to, wave);
     lo.issue(static_cast<const uint16_t *>(g.dout) + row * g.lddo_t + head * g.lddo_h, left, g.lddo_t, a.D, to + kTile, wave);
     if (wave < 2) {  // the rows' log sums, and their sums of dO O
@@ -195,16 +206,17 @@ __global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(RS
   f32x16 dK[DB], dV[DB];
   auto pass = [&](const bool careful) __attribute__((always_inline)) {  // see k_attention
     bool again = false;
-    ih = 0;
-    it = first_tile;
+    ih = per_head > 0 ? begin / per_head : 0;
+    it = first_tile + begin - ih * per_head;
+    int t = it;
 #pragma unroll
     for (int d = 0; d < DB; ++d) dK[d] = dV[d] = zeros16();
-    if (steps > 0) issue(0);
-    int t = first_tile;
-    for (int step = 0; step < steps; ++step) {
+    if (begin < end) issue(0);
+    for (int step = begin; step < end; ++step) {
+      const int buf = (step - begin) & 1;
       tile_barrier();
-      if (step + 1 < steps) issue((step + 1) & 1);
-      const uint8_t *tq = smem + (step & 1) * kStage, *to = tq + kTile;
+      if (step + 1 < end) issue(buf ^ 1);
+      const uint8_t *tq = smem + buf * kStage, *to = tq + kTile;
       const float *rows = reinterpret_cast<const float *>(tq + 2 * kTile);
       const int tile0 = t * kRows;
       t = t + 1 == tiles ? first_tile : t + 1;
@@ -215,90 +227,118 @@ __global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(RS
         again |= apart;
         apart = false;
       }
+      const int i0 = 32 * rs, row0 = tile0 + i0;
+      f32x16 S = zeros16(), dP = zeros16();
 #pragma unroll
-      for (int j = 0; j < 2 / RS; ++j) {
-        const int i = RS == 2 ? rs : j, row0 = tile0 + 32 * i;
-        f32x16 S = zeros16(), dP = zeros16();
+      for (int s = 0; s < KS; ++s) {
+        S = mfma(read.row_operand(tq, i0, s), K[s], S);
+        if constexpr (VL) dP = mfma(read.row_operand(to, i0, s), read.row_operand(tv, 32 * kw, s), dP);
+        else dP = mfma(read.row_operand(to, i0, s), V[s], dP);
+      }
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          S = mfma(read.row_operand(tq, 32 * i, s), K[s], S);
-          dP = mfma(read.row_operand(to, 32 * i, s), V[s], dP);
+      for (int u = 0; u < 4; ++u) {
+        const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(rows + i0 + 8 * u + 4 * h);
+        const f32x4 delta = *reinterpret_cast<const f32x4 *>(rows + kRows + i0 + 8 * u + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          S[4 * u + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * u + e], scale2, -lse2[e]));
+          dP[4 * u + e] = S[4 * u + e] * (dP[4 * u + e] - delta[e]);
         }
+      }
+      if (masked) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(rows + 32 * i + 8 * u + 4 * h);
-          const f32x4 delta = *reinterpret_cast<const f32x4 *>(rows + kRows + 32 * i + 8 * u + 4 * h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            S[4 * u + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * u + e], scale2, -lse2[e]));
-            dP[4 * u + e] = S[4 * u + e] * (dP[4 * u + e] - delta[e]);
-          }
+        for (int r = 0; r < 16; ++r) {
+          const bool in = row0 + c_row(r, h) >= first_row;
+          S[r] = in ? S[r] : 0.0f;
+          dP[r] = in ? dP[r] : 0.0f;
         }
-        if (masked) {
+      }
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const bool in = row0 + c_row(r, h) >= first_row;
-            S[r] = in ? S[r] : 0.0f;
-            dP[r] = in ? dP[r] : 0.0f;
+      for (int s = 0; s < 2; ++s) {
+        const bf16x8 p = as_operand(S, s), ds = as_operand(dP, s);
+        const int r0 = i0 + 16 * s;
+        if (!careful || !apart) {
+#pragma unroll
+          for (int d = 0; d < DB; ++d) {
+            dV[d] = mfma(read.column_operand(to, r0, d), p, dV[d]);
+            dK[d] = mfma(read.column_operand(tq, r0, d), ds, dK[d]);
           }
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const bf16x8 p = as_operand(S, s), ds = as_operand(dP, s);
-          const int r0 = 32 * i + 16 * s;
-          if (!careful || !apart) {
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-              dV[d] = mfma(read.column_operand(to, r0, d), p, dV[d]);
-              dK[d] = mfma(read.column_operand(tq, r0, d), ds, dK[d]);
-            }
-          } else {
-            add_rows_apart<P, DB>(to, r0, p, dV, read, lane, [&](int row) { return tile0 + row >= first_row; });
-            add_rows_apart<P, DB>(tq, r0, ds, dK, read, lane, [&](int row) { return tile0 + row >= first_row; });
-          }
+        } else {
+          add_rows_apart<P, DB>(to, r0, p, dV, read, lane, [&](int row) { return tile0 + row >= first_row; });
+          add_rows_apart<P, DB>(tq, r0, ds, dK, read, lane, [&](int row) { return tile0 + row >= first_row; });
         }
       }
     }
     return again;
   };
   if (__syncthreads_or(pass(false))) pass(true);
-  if constexpr (RS == 2) {  // the second half's sums join the first's
-    f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + kw * (DB * 4 * 64) + lane;
-    auto join = [&](f32x16(&x)[DB]) {
-      __syncthreads();
-      if (rs == 1) {
+  // the second half's sums join the first's
+  f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + kw * (DB * 4 * 64) + lane;
+  auto join = [&](f32x16(&x)[DB]) __attribute__((always_inline)) {
+    __syncthreads();
+    if (rs == 1) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+      for (int d = 0; d < DB; ++d)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) part[(4 * d + u) * 64] = f32x4{x[d][4 * u], x[d][4 * u + 1], x[d][4 * u + 2], x[d][4 * u + 3]};
-      }
-      __syncthreads();
-      if (rs == 0) {
+        for (int u = 0; u < 4; ++u) part[(4 * d + u) * 64] = f32x4{x[d][4 * u], x[d][4 * u + 1], x[d][4 * u + 2], x[d][4 * u + 3]};
+    }
+    __syncthreads();
+    if (rs == 0) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+      for (int d = 0; d < DB; ++d)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const f32x4 o = part[(4 * d + u) * 64];
+        for (int u = 0; u < 4; ++u) {
+          const f32x4 o = part[(4 * d + u) * 64];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[d][4 * u + e] += o[e];
-          }
-      }
-    };
-    join(dK);
-    join(dV);
-    if (rs == 1) return;
-  }
-  if (key >= sk.n) return;
+          for (int e = 0; e < 4; ++e) x[d][4 * u + e] += o[e];
+        }
+    }
+  };
+  join(dK);
+  join(dV);
+  if (rs == 1 || key >= sk.n) return;
   const int64_t row = sk.begin + key;
-  store_column<DB>(dK, a.scale, static_cast<uint16_t *>(g.dk) + row * g.lddk_t + kv * g.lddk_h, a.D, h);
-  store_column<DB>(dV, 1.0f, static_cast<uint16_t *>(g.dv) + row * g.lddv_t + kv * g.lddv_h, a.D, h);
+  if (g.splits == 1) {
+    store_column<DB>(dK, a.scale, static_cast<uint16_t *>(g.dk) + row * g.lddk_t + kv * g.lddk_h, a.D, h);
+    store_column<DB>(dV, 1.0f, static_cast<uint16_t *>(g.dv) + row * g.lddv_t + kv * g.lddv_h, a.D, h);
+  } else {  // [splits][dK, dV][Tk][Hkv][D]
+    const int Hkv = a.Hq / a.group;
+    const int64_t each = (int64_t)a.Tk * Hkv * a.D;
+    float *to = g.parts + 2 * split * each + (row * Hkv + kv) * a.D;
+    store_column_f32<DB>(dK, a.scale, to, a.D, h);
+    store_column_f32<DB>(dV, 1.0f, to + each, a.D, h);
+  }
 }
+
+// Adds the splits of dK (blockIdx.y 0) or dV (1), in order: a thread has 4 values.
+__global__ __launch_bounds__(256) void k_attention_join(const AttentionGradArgs g, const FastDiv per_row, const FastDiv heads) {
+  const AttentionArgs &a = g.f;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t r = fastdiv(i, per_row), at = 4 * (i - r * per_row.d), t = fastdiv(r, heads), head = r - t * heads.d;
+  if (t >= (uint32_t)(a.cu_k ? min(max(a.cu_k[a.B], 0), a.Tk) : a.Tk)) return;
+  const int64_t each = (int64_t)a.Tk * heads.d * a.D;
+  const float *from = g.parts + blockIdx.y * each + (int64_t)r * a.D + at;
+  f32x4 sum = {0, 0, 0, 0};
+  for (int s = 0; s < g.splits; ++s) {
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(from + 2 * s * each);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += x[e];
+  }
+  uint16_t *to = blockIdx.y == 0 ? static_cast<uint16_t *>(g.dk) + t * g.lddk_t + head * g.lddk_h
+                                 : static_cast<uint16_t *>(g.dv) + t * g.lddv_t + head * g.lddv_h;
+  const bf16x2 lo = {(__bf16)sum[0], (__bf16)sum[1]}, hi = {(__bf16)sum[2], (__bf16)sum[3]};
+  *reinterpret_cast<u32x2 *>(to + at) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+}
+
+constexpr int kKeyWaves = 4;
 
 template <int KS, int DB>
 hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
-  constexpr int NW = 4, KW = 4, RS = DB <= 3 ? 2 : 1;
-  constexpr int kTile = kRows * DB * 64, kLdsQ = 4 * kTile, kLdsK = 2 * (2 * kTile + 2 * kRows * 4);
-  static_assert(RS == 1 || KW * DB * 4096 <= kLdsK, "the sums pass through the tiles' memory");
+  constexpr int NW = 4, KW = kKeyWaves;
+  constexpr bool VL = DB == 4;
+  constexpr int kTile = kRows * DB * 64, kLdsQ = 4 * kTile;
+  constexpr int kLdsK = 2 * (2 * kTile + 2 * kRows * 4) + (VL ? 32 * KW * DB * 64 : 0);
+  static_assert(KW * DB * 4096 <= kLdsK, "the sums pass through the tiles' memory");
   static std::atomic<bool> done_q[kMaxDevices], done_k[kMaxDevices];
   if (g.f.Tq > 0) {
     const void *kern = reinterpret_cast<const void *>(&k_attention_dq<KS, DB, NW>);
@@ -307,16 +347,28 @@ hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
     k_attention_dq<KS, DB, NW><<<dim3((unsigned)(g.f.slots * g.f.Hq)), dim3(64 * NW), kLdsQ, stream>>>(g);
   }
   if (g.f.Tk > 0) {
-    const void *kern = reinterpret_cast<const void *>(&k_attention_dkv<KS, DB, KW, RS>);
+    const int Hkv = g.f.Hq / g.f.group;
+    const void *kern = reinterpret_cast<const void *>(&k_attention_dkv<KS, DB, KW, VL>);
     if (hipError_t e = set_dynamic_lds(kern, kLdsK, done_k); e != hipSuccess) return e;
     g.f.slots = (int)attention_slots(g.f.Tk, g.f.B, g.f.cu_k != nullptr, 32 * KW);
-    k_attention_dkv<KS, DB, KW, RS>
-        <<<dim3((unsigned)(g.f.slots * (g.f.Hq / g.f.group))), dim3(64 * KW * RS), kLdsK, stream>>>(g);
+    k_attention_dkv<KS, DB, KW, VL><<<dim3((unsigned)(g.f.slots * Hkv * g.splits)), dim3(128 * KW), kLdsK, stream>>>(g);
+    if (g.splits > 1) {
+      const int64_t threads = (int64_t)g.f.Tk * Hkv * (g.f.D / 4);  // few: the splits are for small problems
+      k_attention_join<<<dim3((unsigned)((threads + 255) / 256), 2), dim3(256), 0, stream>>>(
+          g, make_fastdiv((uint32_t)(g.f.D / 4)), make_fastdiv((uint32_t)Hkv));
+    }
   }
   return hipGetLastError();
 }
 
 }  // namespace
+
+// Workgroups for two rounds of 256 CUs, but none with less than about 4 steps.
+int attention_backward_splits(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t B) {
+  const int64_t blocks = (Tk / (32 * kKeyWaves) + B) * Hkv, want = (512 + blocks - 1) / blocks;
+  const int64_t steps = (Tq / (B > 0 ? B : 1) / kRows + 1) * (Hq / Hkv), most = steps / 4 > 1 ? steps / 4 : 1;
+  return (int)(want < most ? want : most);
+}
 
 hipError_t launch_attention_backward(const AttentionGradArgs &g, hipStream_t stream) {
   const int D = g.f.D;

@@ -212,7 +212,10 @@ struct AttentionGradArgs {  // attention_backward.hip
   void *dq, *dk, *dv;
   int64_t lddq_t, lddq_h, lddk_t, lddk_h, lddv_t, lddv_h;
   float *rows;  // workspace: [2][Hq][Tq], a query's log sum (base 2) and sum of dO O
+  int splits;   // workgroups that share a block of keys; more than one: their fp32 sums go to parts
+  float *parts;
 };
+int attention_backward_splits(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t B);
 hipError_t launch_attention_backward(const AttentionGradArgs &a, hipStream_t stream);
 
 // A paged cache: [pages][Hkv][page][D] of bf16, or of E4M3 codes with scale bytes [pages][Hkv][page][(D + 31) / 32].

@@ -47,6 +47,10 @@ nvfp4_status_t check_attention_shape(int64_t Tq, int64_t Tk, int64_t Hq, int64_t
   return NVFP4_OK;
 }
 
+// the backward pass' two values per query, and whole 16 bytes
+size_t backward_rows_bytes(int64_t Tq, int64_t Hq) { return (2 * sizeof(float) * (size_t)Tq * (size_t)Hq + 15) / 16 * 16; }
+const int32_t *const kAnyOffsets = reinterpret_cast<const int32_t *>(16);  // a packed batch, for size queries
+
 // The shape of a paged cache, and its arrays' extents and alignment.
 nvfp4_status_t check_cache(const void *k, const uint8_t *ks, const void *v, const uint8_t *vs, int64_t pages,
                            int64_t page_size, const int32_t *table, int64_t ld_table, int64_t max_pages,
@@ -98,9 +102,11 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
   return hip_status(launch_attention(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t nvfp4_attention_backward_workspace_bytes(int64_t Tq, int64_t Hq) {
-  if (Tq < 0 || Hq < 0 || Tq >= ((int64_t)1 << 31) || Hq > (1 << 16)) return 0;
-  return 2 * sizeof(float) * (size_t)Tq * (size_t)Hq;
+size_t nvfp4_attention_backward_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, int64_t B) {
+  if (check_attention_shape(Tq, Tk, Hq, Hkv, D, kAnyOffsets, kAnyOffsets, B, 1.0f) != NVFP4_OK || Hq == 0 || B == 0) return 0;
+  const int splits = attention_backward_splits(Tq, Tk, Hq, Hkv, B);
+  const size_t parts = splits > 1 ? 2 * sizeof(float) * (size_t)splits * (size_t)Tk * (size_t)Hkv * (size_t)D : 0;
+  return backward_rows_bytes(Tq, Hq) + parts;
 }
 
 nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, int64_t lddo_head, const void *q,
@@ -127,7 +133,8 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
   for (const Heads &y : grads)
     for (const Heads &x : in)
       if (y.p && y.T > 0 && y.p == x.p) return NVFP4_ERR_STRIDE;
-  if (Tq > 0 && (!workspace || workspace_bytes < nvfp4_attention_backward_workspace_bytes(Tq, Hq)))
+  const size_t need = nvfp4_attention_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, B);
+  if (need > 0 && (!workspace || workspace_bytes < need))
     return NVFP4_ERR_WORKSPACE;
   if (!aligned(lse, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
   if ((st = check_device()) != NVFP4_OK) return st;
@@ -135,7 +142,8 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
                              (int)(Hq / Hkv), (int)D, (int)B, cu_q, cu_k, (int)(Tq / B), (int)(Tk / B), causal != 0, scale,
                              const_cast<void *>(out), ldo_token, ldo_head, const_cast<float *>(lse)},
                             dout, row_pitch(in[0], D), lddo_head, dq, dk, dv, lddq_token, lddq_head, lddk_token, lddk_head,
-                            lddv_token, lddv_head, static_cast<float *>(workspace)};
+                            lddv_token, lddv_head, static_cast<float *>(workspace), attention_backward_splits(Tq, Tk, Hq, Hkv, B),
+                            reinterpret_cast<float *>(static_cast<char *>(workspace) + backward_rows_bytes(Tq, Hq))};
   return hip_status(launch_attention_backward(g, static_cast<hipStream_t>(stream)));
 }
 
