@@ -62,15 +62,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   TileLoad<P, kKeys, NW> lk, lv;
   lk.init(wave, lane, a.ldk_t, a.D);
   lv.init(wave, lane, a.ldv_t, a.D);
-  auto issue = [&](int t, int buf) {
-    uint8_t *at = smem + buf * 2 * kTile;
+  auto issue = [&](int t, uint8_t *at) __attribute__((always_inline)) {
     const int64_t row = (int64_t)t * kKeys;
     const int left = sk.n - t * kKeys;
     lk.issue(k + row * a.ldk_t, left, a.ldk_t, a.D, at, wave);
     lv.issue(v + row * a.ldv_t, left, a.ldv_t, a.D, at + kTile, wave);
   };
 
-  const TileRead<P> read(lane);
+  const TileRead<P> read_(lane);
   const float scale2 = a.scale * kLog2e;  // exp(scale s) = 2^(scale2 s)
   float top, total;  // running maximum of s (both halves of a column), sum (this lane's)
   f32x16 O[DB];
@@ -83,15 +82,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     total = 0.0f;
 #pragma unroll
     for (int d = 0; d < DB; ++d) O[d] = zeros16();
-    if (tiles > 0) issue(0, 0);
-    for (int t = 0; t < tiles; ++t) {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
+    if (tiles > 0) issue(0, smem);
+    auto step = [&](const uint8_t *__restrict cur, uint8_t *__restrict next, int t) __attribute__((always_inline)) {
+      if (t + 1 < tiles) issue(t + 1, next);
       const int key0 = t * kKeys;
-      if (key0 > last_wave) continue;
-      const uint8_t *tk = smem + (t & 1) * 2 * kTile, *tv = tk + kTile;
+      if (key0 > last_wave) return;
+      const TileRead<P> read = read_.here();
+      const uint8_t *tk = cur, *tv = cur + kTile;
 
       f32x16 S[2];
 #pragma unroll
@@ -150,6 +147,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
             add_rows_apart<P, DB>(tv, r0, p, O, read, lane, [&](int row) { return key0 + row <= limit; });
           }
         }
+    };
+    for (int t = 0; t < tiles; ++t) {
+      tile_barrier();
+      step(smem + (t & 1) * 2 * kTile, smem + (~t & 1) * 2 * kTile, t);
     }
     return again;
   };

@@ -55,6 +55,13 @@ __device__ __forceinline__ void find_block(int slot, const int32_t *cu, int B, i
   blk = slot - (min(max(cu[b], 0), T) / BLK + b);
 }
 
+// This wave's loads have landed and its reads of LDS are back, and every other wave's too.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // ---- tiles of head rows in LDS ------------------------------------------------------------------------
 //
 // A tile is ROWS rows of P 16-byte pieces, P = 4 DB (DB blocks of 32 values).  Piece p of row r lies in
@@ -123,6 +130,13 @@ struct TileRead {
     const int r = lane & 31, h = lane >> 5, i = lane & 15, k = 4 * h + (i >> 2);
     rows = r * (P * 16) + ((h ^ swizzle<P>(r)) << 4);
     columns = k * (P * 16) + (((2 * ((lane >> 4) & 1) + ((i >> 1) & 1)) ^ swizzle<P>(k)) << 4) + 8 * (i & 1);
+  }
+  // The same, for use inside a loop: the places of its reads are computed there (one instruction each) instead of
+  // being kept in registers around it.
+  __device__ __forceinline__ TileRead here() const {
+    TileRead r = *this;
+    asm volatile("" : "+v"(r.rows), "+v"(r.columns));
+    return r;
   }
   // A operand: rows r0 .. r0 + 31 (r0 a multiple of 16), values 16 s .. 16 s + 15.
   __device__ __forceinline__ bf16x8 row_operand(const uint8_t *tile, int r0, int s) const {
@@ -243,7 +257,7 @@ __device__ __forceinline__ void add_rows_apart(const uint8_t *tile, int r0, cons
         w[i] = (lane >> 5) == h && e >> 1 == i ? split(w[i], false) & (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
       const f32x16 t = mfma(__builtin_bit_cast(bf16x8, w), b, zeros16());
 #pragma unroll
-      for (int r = 0; r < 16; ++r) c[d][r] = add && t[r] != 0.0f ? c[d][r] + t[r] : c[d][r];
+      for (int r = 0; r < 16; ++r) c[d][r] = (int)add & (int)(t[r] != 0.0f) ? c[d][r] + t[r] : c[d][r];
     }
   }
 }

@@ -14,12 +14,6 @@ namespace {
 
 constexpr int kRows = 64;  // rows per tile
 
-__device__ __forceinline__ void tile_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Heads of the innermost grid: see k_attention.
 __device__ __forceinline__ void block_of(int heads, int slots, bool slots_first, int &head, int &slot) {
   const bool own = heads % 8 == 0;
@@ -79,14 +73,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   TileLoad<P, kRows, NW> lk, lv;
   lk.init(wave, lane, a.ldk_t, a.D);
   lv.init(wave, lane, a.ldv_t, a.D);
-  auto issue = [&](int t, int buf) {
-    uint8_t *to = smem + buf * 2 * kTile;
+  auto issue = [&](int t, uint8_t *to) __attribute__((always_inline)) {
     const int64_t row = (int64_t)t * kRows;
     const int left = sk.n - t * kRows;
     lk.issue(k + row * a.ldk_t, left, a.ldk_t, a.D, to, wave);
     lv.issue(v + row * a.ldv_t, left, a.ldv_t, a.D, to + kTile, wave);
   };
-  const TileRead<P> read(lane);
+  const TileRead<P> read_(lane);
   const float scale2 = a.scale * kLog2e;
   f32x16 dQ[DB];
 
@@ -94,13 +87,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     bool again = false;
 #pragma unroll
     for (int d = 0; d < DB; ++d) dQ[d] = zeros16();
-    if (tiles > 0) issue(0, 0);
-    for (int t = 0; t < tiles; ++t) {
-      tile_barrier();
-      if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
+    if (tiles > 0) issue(0, smem);
+    auto step = [&](const uint8_t *__restrict cur, uint8_t *__restrict next, int t) __attribute__((always_inline)) {
+      if (t + 1 < tiles) issue(t + 1, next);
       const int key0 = t * kRows;
-      if (key0 > last_wave) continue;
-      const uint8_t *tk = smem + (t & 1) * 2 * kTile, *tv = tk + kTile;
+      if (key0 > last_wave) return;
+      const TileRead<P> read = read_.here();
+      const uint8_t *tk = cur, *tv = cur + kTile;
       const bool masked = key0 + kRows - 1 > first_limit;
       bool apart = masked && tile_nonfinite<P, kRows>(tk, lane);
       if (!careful) {
@@ -134,6 +127,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
           }
         }
       }
+    };
+    for (int t = 0; t < tiles; ++t) {
+      tile_barrier();
+      step(smem + (t & 1) * 2 * kTile, smem + (~t & 1) * 2 * kTile, t);
     }
     return again;
   };
@@ -185,8 +182,7 @@ __global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))
   lq.init(wave, lane, a.ldq_t, a.D);
   lo.init(wave, lane, g.lddo_t, a.D);
   int ih, it;  // the next step to load: head of the group, tile
-  auto issue = [&](int buf) {
-    uint8_t *to = smem + buf * kStage;
+  auto issue = [&](uint8_t *to) __attribute__((always_inline)) {
     const int head = kv * a.group + ih;
     const int64_t row = sq.begin + (int64_t)it * kRows;
     const int left = sq.n - it * kRows;
@@ -201,7 +197,7 @@ __global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))
       ++ih;
     }
   };
-  const TileRead<P> read(lane);
+  const TileRead<P> read_(lane);
   const float scale2 = a.scale * kLog2e;
   f32x16 dK[DB], dV[DB];
   auto pass = [&](const bool careful) __attribute__((always_inline)) {  // see k_attention
@@ -211,17 +207,16 @@ __global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))
     int t = it;
 #pragma unroll
     for (int d = 0; d < DB; ++d) dK[d] = dV[d] = zeros16();
-    if (begin < end) issue(0);
-    for (int step = begin; step < end; ++step) {
-      const int buf = (step - begin) & 1;
-      tile_barrier();
-      if (step + 1 < end) issue(buf ^ 1);
-      const uint8_t *tq = smem + buf * kStage, *to = tq + kTile;
+    if (begin < end) issue(smem);
+    auto step = [&](const uint8_t *__restrict cur, uint8_t *__restrict next, int i) __attribute__((always_inline)) {
+      if (i + 1 < end) issue(next);
+      const TileRead<P> read = read_.here();
+      const uint8_t *tq = cur, *to = cur + kTile;
       const float *rows = reinterpret_cast<const float *>(tq + 2 * kTile);
       const int tile0 = t * kRows;
       t = t + 1 == tiles ? first_tile : t + 1;
       const bool masked = tile0 < last_first;
-      if (tile0 + kRows - 1 < first_wave) continue;
+      if (tile0 + kRows - 1 < first_wave) return;
       bool apart = masked && (tile_nonfinite<P, kRows>(tq, lane) || tile_nonfinite<P, kRows>(to, lane));
       if (!careful) {
         again |= apart;
@@ -268,6 +263,10 @@ __global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))
           add_rows_apart<P, DB>(tq, r0, ds, dK, read, lane, [&](int row) { return tile0 + row >= first_row; });
         }
       }
+    };
+    for (int i = begin; i < end; ++i) {
+      tile_barrier();
+      step(smem + ((i - begin) & 1) * kStage, smem + (~(i - begin) & 1) * kStage, i);
     }
     return again;
   };
@@ -335,7 +334,7 @@ constexpr int kKeyWaves = 4;
 template <int KS, int DB>
 hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
   constexpr int NW = 4, KW = kKeyWaves;
-  constexpr bool VL = DB == 4;
+  constexpr bool VL = DB >= 3;
   constexpr int kTile = kRows * DB * 64, kLdsQ = 4 * kTile;
   constexpr int kLdsK = 2 * (2 * kTile + 2 * kRows * 4) + (VL ? 32 * KW * DB * 64 : 0);
   static_assert(KW * DB * 4096 <= kLdsK, "the sums pass through the tiles' memory");
