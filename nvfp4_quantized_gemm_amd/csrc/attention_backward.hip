@@ -139,14 +139,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   store_column<DB>(dQ, a.scale, static_cast<uint16_t *>(g.dq) + (int64_t)(sq.begin + query) * g.lddq_t + head * g.lddq_h, a.D, h);
 }
 
-// KW waves of 32 keys; the two waves of a block of keys take a tile's 32-row halves, and their sums are added at the
-// end.  The steps (query heads of the group, times their tiles) of a block of keys are shared by a.splits workgroups,
+// KW waves of 32 keys (RS = 2: two such sets, which take a tile's 32-row halves and add their sums at the end: with 128
+// values a head one workgroup's tiles fill the LDS of a CU, and its 4 waves would leave the SIMDs one each).  The steps (query heads of the group, times their tiles) of a block of keys are shared by a.splits workgroups,
 // whose sums a second kernel adds.  VL: the value operands are read from LDS at every use (with 128 values a head
 // they would be registers too many for two waves per SIMD).
-template <int KS, int DB, int KW, bool VL>
-__global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attention_dkv(const AttentionGradArgs g) {
+template <int KS, int DB, int KW, int RS, bool VL>
+__global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attention_dkv(const AttentionGradArgs g) {
   const AttentionArgs &a = g.f;
-  constexpr int P = 4 * DB, BK = 32 * KW, NW = 2 * KW, kTile = kRows * P * 16, kStage = 2 * kTile + 2 * kRows * 4;
+  constexpr int P = 4 * DB, BK = 32 * KW, NW = KW * RS, kTile = kRows * P * 16, kStage = 2 * kTile + 512;  // and 64 floats twice: a DMA's
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint8_t *const tv = smem + 2 * kStage;  // VL: the block's values
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))
     lo.issue(static_cast<const uint16_t *>(g.dout) + row * g.lddo_t + head * g.lddo_h, left, g.lddo_t, a.D, to + kTile, wave);
     if (wave < 2) {  // the rows' log sums, and their sums of dO O
       const float *rows = g.rows + ((int64_t)wave * a.Hq + head) * a.Tq + row;
-      buffer_dma4(rows, left > 0 ? 4 * min(left, kRows) : 0, to + 2 * kTile + wave * kRows * 4, 4 * lane);
+      buffer_dma4(rows, left > 0 ? 4 * min(left, kRows) : 0, to + 2 * kTile + 256 * wave, 4 * lane);
     }
     if (++it == tiles) {
       it = first_tile;
@@ -222,45 +222,49 @@ __global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))
         again |= apart;
         apart = false;
       }
-      const int i0 = 32 * rs, row0 = tile0 + i0;
-      f32x16 S = zeros16(), dP = zeros16();
+#pragma unroll 1
+      for (int j = 0; j < 2 / RS; ++j) {
+        const int i0 = 32 * (RS == 2 ? rs : j);
+        const int row0 = tile0 + i0;
+        f32x16 S = zeros16(), dP = zeros16();
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        S = mfma(read.row_operand(tq, i0, s), K[s], S);
-        if constexpr (VL) dP = mfma(read.row_operand(to, i0, s), read.row_operand(tv, 32 * kw, s), dP);
-        else dP = mfma(read.row_operand(to, i0, s), V[s], dP);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(rows + i0 + 8 * u + 4 * h);
-        const f32x4 delta = *reinterpret_cast<const f32x4 *>(rows + kRows + i0 + 8 * u + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          S[4 * u + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * u + e], scale2, -lse2[e]));
-          dP[4 * u + e] = S[4 * u + e] * (dP[4 * u + e] - delta[e]);
+        for (int s = 0; s < KS; ++s) {
+          S = mfma(read.row_operand(tq, i0, s), K[s], S);
+          if constexpr (VL) dP = mfma(read.row_operand(to, i0, s), read.row_operand(tv, 32 * kw, s), dP);
+          else dP = mfma(read.row_operand(to, i0, s), V[s], dP);
         }
-      }
-      if (masked) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const bool in = row0 + c_row(r, h) >= first_row;
-          S[r] = in ? S[r] : 0.0f;
-          dP[r] = in ? dP[r] : 0.0f;
-        }
-      }
+        for (int u = 0; u < 4; ++u) {
+          const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(rows + i0 + 8 * u + 4 * h);
+          const f32x4 delta = *reinterpret_cast<const f32x4 *>(rows + 64 + i0 + 8 * u + 4 * h);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bf16x8 p = as_operand(S, s), ds = as_operand(dP, s);
-        const int r0 = i0 + 16 * s;
-        if (!careful || !apart) {
-#pragma unroll
-          for (int d = 0; d < DB; ++d) {
-            dV[d] = mfma(read.column_operand(to, r0, d), p, dV[d]);
-            dK[d] = mfma(read.column_operand(tq, r0, d), ds, dK[d]);
+          for (int e = 0; e < 4; ++e) {
+            S[4 * u + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * u + e], scale2, -lse2[e]));
+            dP[4 * u + e] = S[4 * u + e] * (dP[4 * u + e] - delta[e]);
           }
-        } else {
-          add_rows_apart<P, DB>(to, r0, p, dV, read, lane, [&](int row) { return tile0 + row >= first_row; });
-          add_rows_apart<P, DB>(tq, r0, ds, dK, read, lane, [&](int row) { return tile0 + row >= first_row; });
+        }
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const bool in = row0 + c_row(r, h) >= first_row;
+            S[r] = in ? S[r] : 0.0f;
+            dP[r] = in ? dP[r] : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const bf16x8 p = as_operand(S, s), ds = as_operand(dP, s);
+          const int r0 = i0 + 16 * s;
+          if (!careful || !apart) {
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              dV[d] = mfma(read.column_operand(to, r0, d), p, dV[d]);
+              dK[d] = mfma(read.column_operand(tq, r0, d), ds, dK[d]);
+            }
+          } else {
+            add_rows_apart<P, DB>(to, r0, p, dV, read, lane, [&](int row) { return tile0 + row >= first_row; });
+            add_rows_apart<P, DB>(tq, r0, ds, dK, read, lane, [&](int row) { return tile0 + row >= first_row; });
+          }
         }
       }
     };
@@ -271,31 +275,33 @@ __global__ __launch_bounds__(128 * KW) __attribute__((amdgpu_waves_per_eu(2, 2))
     return again;
   };
   if (__syncthreads_or(pass(false))) pass(true);
-  // the second half's sums join the first's
-  f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + kw * (DB * 4 * 64) + lane;
-  auto join = [&](f32x16(&x)[DB]) __attribute__((always_inline)) {
-    __syncthreads();
-    if (rs == 1) {
+  if constexpr (RS == 2) {
+    f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + kw * (DB * 4 * 64) + lane;
+    auto join = [&](f32x16(&x)[DB]) __attribute__((always_inline)) {
+      __syncthreads();
+      if (rs == 1) {
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) part[(4 * d + u) * 64] = f32x4{x[d][4 * u], x[d][4 * u + 1], x[d][4 * u + 2], x[d][4 * u + 3]};
-    }
-    __syncthreads();
-    if (rs == 0) {
+          for (int u = 0; u < 4; ++u) part[(4 * d + u) * 64] = f32x4{x[d][4 * u], x[d][4 * u + 1], x[d][4 * u + 2], x[d][4 * u + 3]};
+      }
+      __syncthreads();
+      if (rs == 0) {
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const f32x4 o = part[(4 * d + u) * 64];
+          for (int u = 0; u < 4; ++u) {
+            const f32x4 o = part[(4 * d + u) * 64];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[d][4 * u + e] += o[e];
-        }
-    }
-  };
-  join(dK);
-  join(dV);
-  if (rs == 1 || key >= sk.n) return;
+            for (int e = 0; e < 4; ++e) x[d][4 * u + e] += o[e];
+          }
+      }
+    };
+    join(dK);
+    join(dV);
+    if (rs == 1) return;
+  }
+  if (key >= sk.n) return;
   const int64_t row = sk.begin + key;
   if (g.splits == 1) {
     store_column<DB>(dK, a.scale, static_cast<uint16_t *>(g.dk) + row * g.lddk_t + kv * g.lddk_h, a.D, h);
@@ -336,8 +342,9 @@ hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
   constexpr int NW = 4, KW = kKeyWaves;
   constexpr bool VL = DB >= 3;
   constexpr int kTile = kRows * DB * 64, kLdsQ = 4 * kTile;
-  constexpr int kLdsK = 2 * (2 * kTile + 2 * kRows * 4) + (VL ? 32 * KW * DB * 64 : 0);
-  static_assert(KW * DB * 4096 <= kLdsK, "the sums pass through the tiles' memory");
+  constexpr int RS = DB == 4 ? 2 : 1;
+  constexpr int kLdsK = 2 * (2 * kTile + 512) + (VL ? 32 * KW * DB * 64 : 0);
+  static_assert(RS == 1 || KW * DB * 4096 <= kLdsK, "the sums pass through the tiles' memory");
   static std::atomic<bool> done_q[kMaxDevices], done_k[kMaxDevices];
   if (g.f.Tq > 0) {
     const void *kern = reinterpret_cast<const void *>(&k_attention_dq<KS, DB, NW>);
@@ -347,10 +354,10 @@ hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
   }
   if (g.f.Tk > 0) {
     const int Hkv = g.f.Hq / g.f.group;
-    const void *kern = reinterpret_cast<const void *>(&k_attention_dkv<KS, DB, KW, VL>);
+    const void *kern = reinterpret_cast<const void *>(&k_attention_dkv<KS, DB, KW, RS, VL>);
     if (hipError_t e = set_dynamic_lds(kern, kLdsK, done_k); e != hipSuccess) return e;
     g.f.slots = (int)attention_slots(g.f.Tk, g.f.B, g.f.cu_k != nullptr, 32 * KW);
-    k_attention_dkv<KS, DB, KW, VL><<<dim3((unsigned)(g.f.slots * Hkv * g.splits)), dim3(128 * KW), kLdsK, stream>>>(g);
+    k_attention_dkv<KS, DB, KW, RS, VL><<<dim3((unsigned)(g.f.slots * Hkv * g.splits)), dim3(64 * KW * RS), kLdsK, stream>>>(g);
     if (g.splits > 1) {
       const int64_t threads = (int64_t)g.f.Tk * Hkv * (g.f.D / 4);  // few: the splits are for small problems
       k_attention_join<<<dim3((unsigned)((threads + 255) / 256), 2), dim3(256), 0, stream>>>(
