@@ -478,15 +478,18 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
  *   scale        finite, > 0 (else NVFP4_ERR_MODE).
  *   out          may be q itself (same pitches), and otherwise must not overlap an input.
  *   lse          NULL, or fp32 [Hq][Tq] (the backward pass reads it).
- * Scores, exponentials and sums are fp32; the exponentials are rounded to bf16 for their product with v.
+ *   workspace    nvfp4_attention_workspace_bytes bytes (0 but where there are few queries, whose keys several
+ *                workgroups then share, joined in a fixed order), 16-byte aligned, no initialization.
+ * Equal inputs give equal bits.  Scores, exponentials and sums are fp32; the exponentials are rounded to bf16 for their product with v.
  * Infinities and NaN reach only the queries that attend them.  Tq == 0, Hq == 0 or B == 0 is valid and
  * touches nothing; Tk == 0 writes zeros.
  * ------------------------------------------------------------------------------------------- */
+size_t nvfp4_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, int64_t B);
 nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_head, const void *k, int64_t ldk_token,
                                int64_t ldk_head, const void *v, int64_t ldv_token, int64_t ldv_head, int64_t Tq,
                                int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, const int32_t *cu_q,
                                const int32_t *cu_k, int64_t B, int causal, float scale, void *out, int64_t ldo_token,
-                               int64_t ldo_head, float *lse, void *stream);
+                               int64_t ldo_head, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Its gradients: from dout (the gradient of out) and out and lse as nvfp4_attention wrote them for the same
  * q, k, v, sequences, causal and scale, with delta_i = dout_i . o_i, ds_ij = p_ij (dout_i . v_j - delta_i):
@@ -497,7 +500,7 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
  *   dq, dk, dv      written; at no input's address (NVFP4_ERR_STRIDE) and not overlapping any array.  Rows
  *                   past the last sequence are left as they were; keys that nothing attends get 0.
  *   workspace       nvfp4_attention_backward_workspace_bytes bytes, 16-byte aligned, no initialization (where there
- *                   are few keys, several workgroups share their gradients and add them at the end).
+ *                   are few queries or keys, several workgroups share a gradient and add it at the end).
  * B == 0 or Hq == 0 is valid and touches nothing; Tq == 0 writes dk = dv = 0. */
 size_t nvfp4_attention_backward_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
                                                 int64_t B);

@@ -51,7 +51,7 @@ EXPORTED = (
     "nvfp4_quantize_noalloc", "nvfp4_set_debug_checks",
     "nvfp4_mx8_quantize", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes", "nvfp4_rmsnorm_backward",
     "nvfp4_mx_gemm_w4a8", "nvfp4_rope_axes",
-    "nvfp4_attention", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward",
+    "nvfp4_attention_workspace_bytes", "nvfp4_attention", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward",
     "nvfp4_cache_append", "nvfp4_paged_attention_workspace_bytes", "nvfp4_paged_attention",
 )
 
@@ -147,7 +147,9 @@ def lib():
                                   _vp]
     heads = [_vp, _i64, _i64]  # address, token pitch, head pitch
     L.nvfp4_attention.restype = _i
-    L.nvfp4_attention.argtypes = heads * 3 + [_i64] * 5 + [_vp, _vp, _i64, _i, ctypes.c_float] + heads + [_vp, _vp]
+    L.nvfp4_attention.argtypes = heads * 3 + [_i64] * 5 + [_vp, _vp, _i64, _i, ctypes.c_float] + heads + [_vp, _vp, _sz, _vp]
+    L.nvfp4_attention_workspace_bytes.restype = _sz
+    L.nvfp4_attention_workspace_bytes.argtypes = [_i64] * 6
     L.nvfp4_attention_backward_workspace_bytes.restype = _sz
     L.nvfp4_attention_backward_workspace_bytes.argtypes = [_i64] * 6
     L.nvfp4_attention_backward.restype = _i
@@ -846,9 +848,25 @@ def _offsets(cu_q, cu_k, batch: int, dev: int):
     return _dense(cu_q, "cu_q", n, _i32, dev), _dense(cu_k, "cu_k", n, _i32, dev), n[0] - 1
 
 
+def _workspace(given, need: int, ref: torch.Tensor, dev: int):
+    """(tensor to keep until the launch, its address, bytes) of a call's scratch memory: the given one, or a new one."""
+    if given is None:
+        if not need:
+            return None, 0, 0
+        given = torch.empty(need, dtype=_u8, device=ref.device)
+        return given, given.data_ptr(), need
+    if given.get_device() != dev or not given.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}, got one on {given.device}")
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def nvfp4_attention_workspace_bytes(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, batch: int) -> int:
+    return int(lib().nvfp4_attention_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch))
+
+
 def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False, scale: float | None = None,
                     cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, batch: int = 1,
-                    save_lse: bool = False, out=None, lse=None, stream=None):
+                    save_lse: bool = False, out=None, lse=None, workspace=None, stream=None):
     """Softmax attention of q [Tq, Hq, D] over k, v [Tk, Hkv, D] (bf16, token strides from D on and head strides free: views
     of a QKV output are read in place).  Hq is a multiple of Hkv.  Returns (out, lse): out bf16 [Tq, Hq, D], lse fp32 [Hq, Tq], the
     log sums of exponentials that the backward pass reads (None without save_lse or a given lse).
@@ -859,7 +877,7 @@ def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal
     if stream is not None:
         with torch.cuda.stream(stream):
             return nvfp4_attention(q, k, v, causal=causal, scale=scale, cu_q=cu_q, cu_k=cu_k, batch=batch,
-                                   save_lse=save_lse, out=out, lse=lse)
+                                   save_lse=save_lse, out=out, lse=lse, workspace=workspace)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [T, H, D]")
     Tq, Hq, D = shape = q.shape
@@ -883,9 +901,10 @@ def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal
         lse = torch.empty(Hq, Tq, dtype=_f32, device=q.device) if p_cq == 0 else \
             torch.full((Hq, Tq), -math.inf, dtype=_f32, device=q.device)
         p_l = lse.data_ptr()
-    st = lib().nvfp4_attention(p_q, qt, qh, p_k, kt, kh, p_v, vt, vh, Tq, Tk, Hq, Hkv, D, p_cq, p_ck, batch,
-                               1 if causal else 0, D ** -0.5 if scale is None else scale, p_o, ot, oh, p_l,
-                               _current_stream(dev))
+    L = lib()
+    workspace, p_w, n = _workspace(workspace, L.nvfp4_attention_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch), q, dev)
+    st = L.nvfp4_attention(p_q, qt, qh, p_k, kt, kh, p_v, vt, vh, Tq, Tk, Hq, Hkv, D, p_cq, p_ck, batch, 1 if causal else 0,
+                           D ** -0.5 if scale is None else scale, p_o, ot, oh, p_l, p_w, n, _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_attention")
     return out, lse
@@ -924,17 +943,11 @@ def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
             _written(t, name)
         grads.append(t)
     L = lib()
-    if workspace is None:
-        n = L.nvfp4_attention_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch)
-        workspace = torch.empty(n, dtype=_u8, device=q.device)
-    elif workspace.get_device() != dev:
-        raise ValueError(f"workspace is on {workspace.device}, not on {q.device}")
-    else:
-        n = workspace.numel() * workspace.element_size()
+    workspace, p_w, n = _workspace(workspace, L.nvfp4_attention_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch), q, dev)
     st = L.nvfp4_attention_backward(*args, Tq, Tk, Hq, Hkv, D, p_cq, p_ck, batch, 1 if causal else 0,
                                     D ** -0.5 if scale is None else scale, *_heads(grads[0], "dq", shape_q, dev),
                                     *_heads(grads[1], "dk", shape_k, dev), *_heads(grads[2], "dv", shape_k, dev),
-                                    workspace.data_ptr(), n, _current_stream(dev))
+                                    p_w, n, _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_attention_backward")
     return tuple(grads)
@@ -1065,16 +1078,7 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.
         p_o, ot, oh = _heads(out, "out", shape, dev)
         _written(out, "out")
     L = lib()
-    if workspace is None:
-        n = L.nvfp4_paged_attention_workspace_bytes(B, Hq, Hkv, D, most * size)
-        p_w = 0
-        if n:
-            workspace = torch.empty(n, dtype=_u8, device=q.device)
-            p_w = workspace.data_ptr()
-    elif workspace.get_device() != dev:
-        raise ValueError(f"workspace is on {workspace.device}, not on {q.device}")
-    else:
-        p_w, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    workspace, p_w, n = _workspace(workspace, L.nvfp4_paged_attention_workspace_bytes(B, Hq, Hkv, D, most * size), q, dev)
     st = L.nvfp4_paged_attention(p_q, qt, qh, B, Hq, Hkv, D, ck, cks, cv, cvs, pages, size, table, ld, most,
                                  lengths.data_ptr(), D ** -0.5 if scale is None else scale, p_o, ot, oh, p_w, n,
                                  _current_stream(dev))
@@ -1096,6 +1100,6 @@ __all__ = [
     "nvfp4_mx8_quantize", "RMSNormOutput", "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward_workspace_bytes",
     "nvfp4_rmsnorm_backward", "rmsnorm", "nvfp4_mx_gemm_w4a8",
     "ROPE_PAIRS", "ROPE_HALVES", "rope_inv_freq", "nvfp4_rope_axes", "rope_axes",
-    "nvfp4_attention", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward", "attention",
+    "nvfp4_attention_workspace_bytes", "nvfp4_attention", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward", "attention",
     "PagedCache", "paged_cache", "nvfp4_cache_append", "nvfp4_paged_attention_workspace_bytes", "nvfp4_paged_attention",
 ]

@@ -23,22 +23,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // Which block of which head: neighbouring workgroups lie on different XCDs, so where the heads divide
-  // evenly each XCD takes its own, and all blocks that read a key head's rows share an L2.  Causal blocks
-  // with many keys first.
   int head, slot;
-  {
-    const int items = a.slots * a.Hq, w = blockIdx.x;
-    const int per = a.Hq % 8 == 0 ? a.Hq / 8 : a.Hq, i = a.Hq % 8 == 0 ? w >> 3 : w, x = a.Hq % 8 == 0 ? (w & 7) * per : 0;
-    (void)items;
-    if (a.causal) {
-      slot = a.slots - 1 - i / per;
-      head = x + i % per;
-    } else {
-      head = x + i / a.slots;
-      slot = i % a.slots;
-    }
-  }
+  block_of(a.Hq, a.slots * a.splits, a.causal, head, slot);
+  if (a.causal) slot = a.slots * a.splits - 1 - slot;
+  const int split = slot % a.splits;
+  slot /= a.splits;
   int b, blk;
   find_block<BQ>(slot, a.cu_q, a.B, a.Tq, a.per_q, lane, b, blk);
   const SeqRows sq = seq_rows(a.cu_q, b, a.Tq, a.per_q), sk = seq_rows(a.cu_k, b, a.Tk, a.per_k);
@@ -57,7 +46,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int last_wg = a.causal ? min(min((blk + 1) * BQ, sq.n) - 1 + ahead, sk.n - 1) : sk.n - 1;
   const int last_wave = a.causal ? min(q0 + 31 + ahead, sk.n - 1) : sk.n - 1;
   const int first_limit = a.causal ? min(q0 + ahead, sk.n - 1) : sk.n - 1;
-  const int tiles = q0 - 32 * wave < sq.n && last_wg >= 0 ? last_wg / kKeys + 1 : 0;
+  const int all = last_wg >= 0 ? last_wg / kKeys + 1 : 0;
+  const int first = (int)((int64_t)all * split / a.splits), tiles = (int)((int64_t)all * (split + 1) / a.splits);
 
   TileLoad<P, kKeys, NW> lk, lv;
   lk.init(wave, lane, a.ldk_t, a.D);
@@ -82,7 +72,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     total = 0.0f;
 #pragma unroll
     for (int d = 0; d < DB; ++d) O[d] = zeros16();
-    if (tiles > 0) issue(0, smem);
+    if (first < tiles) issue(first, smem);
     auto step = [&](const uint8_t *__restrict cur, uint8_t *__restrict next, int t) __attribute__((always_inline)) {
       if (t + 1 < tiles) issue(t + 1, next);
       const int key0 = t * kKeys;
@@ -128,7 +118,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
           S[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i][r], scale2, -shift));
           total += S[i][r];
         }
-      bool apart = masked && tile_nonfinite<P, kKeys>(tv, lane);
+      bool apart = masked && a.causal && tile_nonfinite<P, kKeys>(tv, lane);
       if (!careful) {
         again |= apart;
         apart = false;
@@ -148,9 +138,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
           }
         }
     };
-    for (int t = 0; t < tiles; ++t) {
+    for (int t = first; t < tiles; ++t) {
       tile_barrier();
-      step(smem + (t & 1) * 2 * kTile, smem + (~t & 1) * 2 * kTile, t);
+      step(smem + ((t - first) & 1) * 2 * kTile, smem + (~(t - first) & 1) * 2 * kTile, t);
     }
     return again;
   };
@@ -158,39 +148,81 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 
   total = add_halves(total);
   if (query >= sq.n) return;
+  const int64_t row = sq.begin + query;
+  if (a.splits > 1) {  // [splits][Tq][Hq][D] sums relative to 2^top, then [splits][Tq][Hq] (top, sum of weights)
+    const int64_t each = (int64_t)a.Tq * a.Hq, at = split * each + row * a.Hq + head;
+    store_column_f32<DB>(O, 1.0f, a.parts + at * a.D, a.D, h);
+    if (h == 0) reinterpret_cast<f32x2 *>(a.parts + a.splits * each * a.D)[at] = f32x2{top * scale2, total};
+    return;
+  }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // a query without keys: 0
-  uint16_t *out = static_cast<uint16_t *>(a.out) + (int64_t)(sq.begin + query) * a.ldo_t + head * a.ldo_h;
-  store_column<DB>(O, inv, out, a.D, h);
+  store_column<DB>(O, inv, static_cast<uint16_t *>(a.out) + row * a.ldo_t + head * a.ldo_h, a.D, h);
   if (a.lse && h == 0)
-    a.lse[(int64_t)head * a.Tq + sq.begin + query] =
-        total == 0.0f ? -INFINITY : (top * scale2 + __builtin_amdgcn_logf(total)) * kLn2;
+    a.lse[(int64_t)head * a.Tq + row] = total == 0.0f ? -INFINITY : (top * scale2 + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
-template <int KS, int DB, int NW>
+// Joins the splits in order: a thread has 4 values of a query's head.
+__global__ __launch_bounds__(256) void k_attention_join(const AttentionArgs a, const FastDiv per_row, const FastDiv heads) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x, r = fastdiv(i, per_row), d = 4 * (i - r * per_row.d);
+  const uint32_t t = fastdiv(r, heads), head = r - t * heads.d;
+  if (t >= (uint32_t)rows_in_use(a.cu_q, a.B, a.Tq)) return;
+  const int64_t each = (int64_t)a.Tq * a.Hq;
+  const f32x2 *const st = reinterpret_cast<const f32x2 *>(a.parts + a.splits * each * a.D) + r;
+  float top = -INFINITY, total = 0.0f;
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, st[s * each].x);
+  f32x4 o = {0, 0, 0, 0};
+  for (int s = 0; s < a.splits; ++s) {
+    const f32x2 x = st[s * each];
+    const float f = x.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);
+    const f32x4 v = *reinterpret_cast<const f32x4 *>(a.parts + (s * each + r) * a.D + d);
+    total += x.y * f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += v[e] * f;
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const bf16x2 lo = {(__bf16)(o[0] * inv), (__bf16)(o[1] * inv)}, hi = {(__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
+  *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + t * a.ldo_t + head * a.ldo_h + d) =
+      u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+  if (a.lse && d == 0)
+    a.lse[(int64_t)head * a.Tq + t] = total == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+constexpr int kWaves = 4;
+
+template <int KS, int DB>
 hipError_t launch(AttentionArgs a, hipStream_t stream) {
   constexpr int kLds = 4 * kKeys * DB * 64;
   static std::atomic<bool> done[kMaxDevices];
-  const void *kern = reinterpret_cast<const void *>(&k_attention<KS, DB, NW>);
+  const void *kern = reinterpret_cast<const void *>(&k_attention<KS, DB, kWaves>);
   if (hipError_t e = set_dynamic_lds(kern, kLds, done); e != hipSuccess) return e;
-  a.slots = (int)attention_slots(a.Tq, a.B, a.cu_q != nullptr, 32 * NW);
-  k_attention<KS, DB, NW><<<dim3((unsigned)(a.slots * a.Hq)), dim3(64 * NW), kLds, stream>>>(a);
+  a.slots = (int)attention_slots(a.Tq, a.B, a.cu_q != nullptr, 32 * kWaves);
+  k_attention<KS, DB, kWaves><<<dim3((unsigned)(a.slots * a.Hq * a.splits)), dim3(64 * kWaves), kLds, stream>>>(a);
+  if (a.splits > 1) {
+    const int64_t threads = (int64_t)a.Tq * a.Hq * (a.D / 4);  // few: the splits are for small problems
+    k_attention_join<<<dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream>>>(a, make_fastdiv((uint32_t)(a.D / 4)),
+                                                                                      make_fastdiv((uint32_t)a.Hq));
+  }
   return hipGetLastError();
-}
-
-template <int KS, int DB>
-hipError_t launch_waves(const AttentionArgs &a, hipStream_t stream) {
-  return launch<KS, DB, 4>(a, stream);
 }
 
 }  // namespace
 
+// Workgroups that share a block of queries' keys: for one on each of 256 CUs, none with less than four tiles (256 keys).
+// Alone a workgroup takes 0.95 us a tile: 17 queries x 32 heads over 4096 keys 77 us, shared by 8 22 us; 926 x 4 heads over
+// 1933 36 and 21; but 1024 x 16 heads, 144 workgroups, 23 us, and 26 shared by 3: their fp32 sums go through memory.
+int attention_splits(int64_t Tq, int64_t Tk, int64_t Hq, int64_t B) {
+  const int64_t blocks = (Tq / (32 * kWaves) + B) * Hq, want = 256 / (blocks > 0 ? blocks : 1);
+  const int64_t most = Tk / (B > 0 ? B : 1) / (4 * kKeys), n = want < most ? want : most;
+  return (int)(n < 1 ? 1 : n < 32 ? n : 32);
+}
+
 hipError_t launch_attention(const AttentionArgs &a, hipStream_t stream) {
-  if (a.D <= 32) return launch_waves<2, 1>(a, stream);
-  if (a.D <= 64) return launch_waves<4, 2>(a, stream);
-  if (a.D <= 80) return launch_waves<5, 3>(a, stream);
-  if (a.D <= 96) return launch_waves<6, 3>(a, stream);
-  if (a.D <= 112) return launch_waves<7, 4>(a, stream);
-  return launch_waves<8, 4>(a, stream);
+  if (a.D <= 32) return launch<2, 1>(a, stream);
+  if (a.D <= 64) return launch<4, 2>(a, stream);
+  if (a.D <= 80) return launch<5, 3>(a, stream);
+  if (a.D <= 96) return launch<6, 3>(a, stream);
+  if (a.D <= 112) return launch<7, 4>(a, stream);
+  return launch<8, 4>(a, stream);
 }
 
 }  // namespace nvfp4

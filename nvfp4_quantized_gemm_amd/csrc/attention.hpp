@@ -55,6 +55,24 @@ __device__ __forceinline__ void find_block(int slot, const int32_t *cu, int B, i
   blk = slot - (min(max(cu[b], 0), T) / BLK + b);
 }
 
+// Rows of all sequences together.
+__device__ __forceinline__ int rows_in_use(const int32_t *cu, int B, int T) { return cu ? min(max(cu[B], 0), T) : T; }
+
+// Which block of which head: neighbouring workgroups lie on different XCDs, so where the heads divide evenly
+// each XCD takes its own, and all blocks that read a key head's rows share an L2.  slots_first: block by block
+// over the heads (causal blocks with many tiles go first), else head by head.
+__device__ __forceinline__ void block_of(int heads, int slots, bool slots_first, int &head, int &slot) {
+  const bool own = heads % 8 == 0;
+  const int w = blockIdx.x, per = own ? heads / 8 : heads, i = own ? w >> 3 : w, x = own ? (w & 7) * per : 0;
+  if (slots_first) {
+    slot = i / per;
+    head = x + i % per;
+  } else {
+    head = x + i / slots;
+    slot = i % slots;
+  }
+}
+
 // This wave's loads have landed and its reads of LDS are back, and every other wave's too.
 __device__ __forceinline__ void tile_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");

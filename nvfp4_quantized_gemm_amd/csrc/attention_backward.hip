@@ -14,19 +14,6 @@ namespace {
 
 constexpr int kRows = 64;  // rows per tile
 
-// Heads of the innermost grid: see k_attention.
-__device__ __forceinline__ void block_of(int heads, int slots, bool slots_first, int &head, int &slot) {
-  const bool own = heads % 8 == 0;
-  const int w = blockIdx.x, per = own ? heads / 8 : heads, i = own ? w >> 3 : w, x = own ? (w & 7) * per : 0;
-  if (slots_first) {
-    slot = i / per;
-    head = x + i % per;
-  } else {
-    head = x + i / slots;
-    slot = i % slots;
-  }
-}
-
 template <int KS, int DB, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_attention_dq(const AttentionGradArgs g) {
   const AttentionArgs &a = g.f;
@@ -35,8 +22,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int head, slot, b, blk;
-  block_of(a.Hq, a.slots, a.causal, head, slot);
-  if (a.causal) slot = a.slots - 1 - slot;
+  block_of(a.Hq, a.slots * a.splits, a.causal, head, slot);
+  if (a.causal) slot = a.slots * a.splits - 1 - slot;
+  const int split = slot % a.splits;
+  slot /= a.splits;
   find_block<BQ>(slot, a.cu_q, a.B, a.Tq, a.per_q, lane, b, blk);
   const SeqRows sq = seq_rows(a.cu_q, b, a.Tq, a.per_q), sk = seq_rows(a.cu_k, b, a.Tk, a.per_k);
   if (blk < 0 || blk * BQ >= sq.n) return;
@@ -60,7 +49,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   delta = add_halves(delta);
   const int64_t at = (int64_t)head * a.Tq + sq.begin + query;
   const float lse2 = query < sq.n ? a.lse[at] * kLog2e : 0.0f;
-  if (query < sq.n && h == 0) {
+  if (query < sq.n && h == 0 && split == 0) {
     g.rows[at] = lse2;
     g.rows[(int64_t)a.Hq * a.Tq + at] = delta;
   }
@@ -69,7 +58,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int last_wg = a.causal ? min(min((blk + 1) * BQ, sq.n) - 1 + ahead, sk.n - 1) : sk.n - 1;
   const int last_wave = a.causal ? min(q0 + 31 + ahead, sk.n - 1) : sk.n - 1;
   const int first_limit = a.causal ? min(q0 + ahead, sk.n - 1) : sk.n - 1;
-  const int tiles = last_wg >= 0 ? last_wg / kRows + 1 : 0;
+  const int all = last_wg >= 0 ? last_wg / kRows + 1 : 0;
+  const int first = (int)((int64_t)all * split / a.splits), tiles = (int)((int64_t)all * (split + 1) / a.splits);
   TileLoad<P, kRows, NW> lk, lv;
   lk.init(wave, lane, a.ldk_t, a.D);
   lv.init(wave, lane, a.ldv_t, a.D);
@@ -87,7 +77,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     bool again = false;
 #pragma unroll
     for (int d = 0; d < DB; ++d) dQ[d] = zeros16();
-    if (tiles > 0) issue(0, smem);
+    if (first < tiles) issue(first, smem);
     auto step = [&](const uint8_t *__restrict cur, uint8_t *__restrict next, int t) __attribute__((always_inline)) {
       if (t + 1 < tiles) issue(t + 1, next);
       const int key0 = t * kRows;
@@ -95,7 +85,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
       const TileRead<P> read = read_.here();
       const uint8_t *tk = cur, *tv = cur + kTile;
       const bool masked = key0 + kRows - 1 > first_limit;
-      bool apart = masked && tile_nonfinite<P, kRows>(tk, lane);
+      bool apart = masked && a.causal && tile_nonfinite<P, kRows>(tk, lane);
       if (!careful) {
         again |= apart;
         apart = false;
@@ -128,14 +118,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
         }
       }
     };
-    for (int t = 0; t < tiles; ++t) {
+    for (int t = first; t < tiles; ++t) {
       tile_barrier();
-      step(smem + (t & 1) * 2 * kTile, smem + (~t & 1) * 2 * kTile, t);
+      step(smem + ((t - first) & 1) * 2 * kTile, smem + (~(t - first) & 1) * 2 * kTile, t);
     }
     return again;
   };
   if (__syncthreads_or(pass(false))) pass(true);
   if (query >= sq.n) return;
+  if (a.splits > 1) {  // [splits][Tq][Hq][D]
+    store_column_f32<DB>(dQ, a.scale, a.parts + (((int64_t)split * a.Tq + sq.begin + query) * a.Hq + head) * a.D, a.D, h);
+    return;
+  }
   store_column<DB>(dQ, a.scale, static_cast<uint16_t *>(g.dq) + (int64_t)(sq.begin + query) * g.lddq_t + head * g.lddq_h, a.D, h);
 }
 
@@ -309,30 +303,40 @@ __global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(2,
   } else {  // [splits][dK, dV][Tk][Hkv][D]
     const int Hkv = a.Hq / a.group;
     const int64_t each = (int64_t)a.Tk * Hkv * a.D;
-    float *to = g.parts + 2 * split * each + (row * Hkv + kv) * a.D;
+    float *to = a.parts + 2 * split * each + (row * Hkv + kv) * a.D;
     store_column_f32<DB>(dK, a.scale, to, a.D, h);
     store_column_f32<DB>(dV, 1.0f, to + each, a.D, h);
   }
 }
 
-// Adds the splits of dK (blockIdx.y 0) or dV (1), in order: a thread has 4 values.
-__global__ __launch_bounds__(256) void k_attention_join(const AttentionGradArgs g, const FastDiv per_row, const FastDiv heads) {
-  const AttentionArgs &a = g.f;
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t r = fastdiv(i, per_row), at = 4 * (i - r * per_row.d), t = fastdiv(r, heads), head = r - t * heads.d;
-  if (t >= (uint32_t)(a.cu_k ? min(max(a.cu_k[a.B], 0), a.Tk) : a.Tk)) return;
-  const int64_t each = (int64_t)a.Tk * heads.d * a.D;
-  const float *from = g.parts + blockIdx.y * each + (int64_t)r * a.D + at;
+// Adds fp32 parts [splits][outputs][T][H][D] in order: a thread has 4 values of output blockIdx.y.
+struct GradJoin {
+  const float *parts;
+  int splits, T, D, B;
+  const int32_t *cu;
+  void *out[2];
+  int64_t ld_t[2], ld_h[2];
+  FastDiv per_row, heads;
+};
+__global__ __launch_bounds__(256) void k_gradient_join(const GradJoin g) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x, j = blockIdx.y;
+  const uint32_t r = fastdiv(i, g.per_row), at = 4 * (i - r * g.per_row.d), t = fastdiv(r, g.heads), head = r - t * g.heads.d;
+  if (t >= (uint32_t)rows_in_use(g.cu, g.B, g.T)) return;
+  const int64_t each = (int64_t)g.T * g.heads.d * g.D;
+  const float *from = g.parts + j * each + (int64_t)r * g.D + at;
   f32x4 sum = {0, 0, 0, 0};
   for (int s = 0; s < g.splits; ++s) {
-    const f32x4 x = *reinterpret_cast<const f32x4 *>(from + 2 * s * each);
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(from + gridDim.y * s * each);
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] += x[e];
   }
-  uint16_t *to = blockIdx.y == 0 ? static_cast<uint16_t *>(g.dk) + t * g.lddk_t + head * g.lddk_h
-                                 : static_cast<uint16_t *>(g.dv) + t * g.lddv_t + head * g.lddv_h;
   const bf16x2 lo = {(__bf16)sum[0], (__bf16)sum[1]}, hi = {(__bf16)sum[2], (__bf16)sum[3]};
-  *reinterpret_cast<u32x2 *>(to + at) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+  *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(g.out[j]) + t * g.ld_t[j] + head * g.ld_h[j] + at) =
+      u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+}
+void join(const GradJoin &g, int outputs, hipStream_t stream) {
+  const int64_t threads = (int64_t)g.T * g.heads.d * (g.D / 4);  // few: the splits are for small problems
+  k_gradient_join<<<dim3((unsigned)((threads + 255) / 256), (unsigned)outputs), dim3(256), 0, stream>>>(g);
 }
 
 constexpr int kKeyWaves = 4;
@@ -346,23 +350,25 @@ hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
   constexpr int kLdsK = 2 * (2 * kTile + 512) + (VL ? 32 * KW * DB * 64 : 0);
   static_assert(RS == 1 || KW * DB * 4096 <= kLdsK, "the sums pass through the tiles' memory");
   static std::atomic<bool> done_q[kMaxDevices], done_k[kMaxDevices];
+  const int Hkv = g.f.Hq / g.f.group;
+  const FastDiv per_row = make_fastdiv((uint32_t)(g.f.D / 4));
   if (g.f.Tq > 0) {
     const void *kern = reinterpret_cast<const void *>(&k_attention_dq<KS, DB, NW>);
     if (hipError_t e = set_dynamic_lds(kern, kLdsQ, done_q); e != hipSuccess) return e;
     g.f.slots = (int)attention_slots(g.f.Tq, g.f.B, g.f.cu_q != nullptr, 32 * NW);
-    k_attention_dq<KS, DB, NW><<<dim3((unsigned)(g.f.slots * g.f.Hq)), dim3(64 * NW), kLdsQ, stream>>>(g);
+    k_attention_dq<KS, DB, NW><<<dim3((unsigned)(g.f.slots * g.f.Hq * g.f.splits)), dim3(64 * NW), kLdsQ, stream>>>(g);
+    if (g.f.splits > 1)
+      join({g.f.parts, g.f.splits, g.f.Tq, g.f.D, g.f.B, g.f.cu_q, {g.dq, nullptr}, {g.lddq_t, 0}, {g.lddq_h, 0}, per_row,
+            make_fastdiv((uint32_t)g.f.Hq)}, 1, stream);
   }
   if (g.f.Tk > 0) {
-    const int Hkv = g.f.Hq / g.f.group;
     const void *kern = reinterpret_cast<const void *>(&k_attention_dkv<KS, DB, KW, RS, VL>);
     if (hipError_t e = set_dynamic_lds(kern, kLdsK, done_k); e != hipSuccess) return e;
     g.f.slots = (int)attention_slots(g.f.Tk, g.f.B, g.f.cu_k != nullptr, 32 * KW);
     k_attention_dkv<KS, DB, KW, RS, VL><<<dim3((unsigned)(g.f.slots * Hkv * g.splits)), dim3(64 * KW * RS), kLdsK, stream>>>(g);
-    if (g.splits > 1) {
-      const int64_t threads = (int64_t)g.f.Tk * Hkv * (g.f.D / 4);  // few: the splits are for small problems
-      k_attention_join<<<dim3((unsigned)((threads + 255) / 256), 2), dim3(256), 0, stream>>>(
-          g, make_fastdiv((uint32_t)(g.f.D / 4)), make_fastdiv((uint32_t)Hkv));
-    }
+    if (g.splits > 1)
+      join({g.f.parts, g.splits, g.f.Tk, g.f.D, g.f.B, g.f.cu_k, {g.dk, g.dv}, {g.lddk_t, g.lddv_t}, {g.lddk_h, g.lddv_h}, per_row,
+            make_fastdiv((uint32_t)Hkv)}, 2, stream);
   }
   return hipGetLastError();
 }

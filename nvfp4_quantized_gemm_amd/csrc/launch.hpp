@@ -201,19 +201,21 @@ struct AttentionArgs {  // attention.hip; all bf16 but lse; pitches in elements,
   float scale;
   void *out;
   int64_t ldo_t, ldo_h;
-  float *lse;     // [Hq][Tq] or null
+  float *lse;      // [Hq][Tq] or null
+  int splits;      // workgroups that share a block of queries' keys; more than one: their fp32 sums go to parts
+  float *parts;
   int slots = 0;  // blocks of rows; the launcher sets it
 };
+int attention_splits(int64_t Tq, int64_t Tk, int64_t Hq, int64_t B);
 hipError_t launch_attention(const AttentionArgs &a, hipStream_t stream);
 struct AttentionGradArgs {  // attention_backward.hip
-  AttentionArgs f;          // out and lse as the forward call wrote them
+  AttentionArgs f;  // out and lse as the forward call wrote them; splits and parts are those of dq
   const void *dout;
   int64_t lddo_t, lddo_h;
   void *dq, *dk, *dv;
   int64_t lddq_t, lddq_h, lddk_t, lddk_h, lddv_t, lddv_h;
   float *rows;  // workspace: [2][Hq][Tq], a query's log sum (base 2) and sum of dO O
-  int splits;   // workgroups that share a block of keys; more than one: their fp32 sums go to parts
-  float *parts;
+  int splits;   // workgroups that share a block of keys' queries; parts are f's
 };
 int attention_backward_splits(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t B);
 hipError_t launch_attention_backward(const AttentionGradArgs &a, hipStream_t stream);

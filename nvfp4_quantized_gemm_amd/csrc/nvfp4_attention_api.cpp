@@ -80,11 +80,17 @@ PagedCacheArgs cache_args(const void *k, const uint8_t *ks, const void *v, const
 
 extern "C" {
 
+size_t nvfp4_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, int64_t B) {
+  if (check_attention_shape(Tq, Tk, Hq, Hkv, D, kAnyOffsets, kAnyOffsets, B, 1.0f) != NVFP4_OK || Hq == 0 || B == 0) return 0;
+  const int splits = attention_splits(Tq, Tk, Hq, B);
+  return splits > 1 ? sizeof(float) * (size_t)splits * (size_t)Tq * (size_t)Hq * (size_t)(D + 2) : 0;
+}
+
 nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_head, const void *k, int64_t ldk_token,
                                int64_t ldk_head, const void *v, int64_t ldv_token, int64_t ldv_head, int64_t Tq,
                                int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, const int32_t *cu_q,
                                const int32_t *cu_k, int64_t B, int causal, float scale, void *out, int64_t ldo_token,
-                               int64_t ldo_head, float *lse, void *stream) {
+                               int64_t ldo_head, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
   nvfp4_status_t st = check_attention_shape(Tq, Tk, Hq, Hkv, D, cu_q, cu_k, B, scale);
   if (st != NVFP4_OK) return st;
   if (Tq == 0 || Hq == 0 || B == 0) return NVFP4_OK;
@@ -94,19 +100,22 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
       (st = check_heads(hv, D, false)) != NVFP4_OK || (st = check_heads(ho, D, true)) != NVFP4_OK)
     return st;
   if (!same_place_fits(ho, hq)) return NVFP4_ERR_STRIDE;
-  if (!aligned(lse, 4)) return NVFP4_ERR_ALIGN;
+  const size_t need = nvfp4_attention_workspace_bytes(Tq, Tk, Hq, Hkv, D, B);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(lse, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
   if ((st = check_device()) != NVFP4_OK) return st;
   const AttentionArgs a{q, k, v, row_pitch(hq, D), ldq_head, row_pitch(hk, D), ldk_head, row_pitch(hv, D), ldv_head, (int)Tq, (int)Tk, (int)Hq,
                         (int)(Hq / Hkv), (int)D, (int)B, cu_q, cu_k, (int)(Tq / B), (int)(Tk / B), causal != 0, scale, out,
-                        ldo_token, ldo_head, lse};
+                        ldo_token, ldo_head, lse, attention_splits(Tq, Tk, Hq, B), static_cast<float *>(workspace)};
   return hip_status(launch_attention(a, static_cast<hipStream_t>(stream)));
 }
 
 size_t nvfp4_attention_backward_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, int64_t B) {
   if (check_attention_shape(Tq, Tk, Hq, Hkv, D, kAnyOffsets, kAnyOffsets, B, 1.0f) != NVFP4_OK || Hq == 0 || B == 0) return 0;
-  const int splits = attention_backward_splits(Tq, Tk, Hq, Hkv, B);
-  const size_t parts = splits > 1 ? 2 * sizeof(float) * (size_t)splits * (size_t)Tk * (size_t)Hkv * (size_t)D : 0;
-  return backward_rows_bytes(Tq, Hq) + parts;
+  const int dq = attention_splits(Tq, Tk, Hq, B), dkv = attention_backward_splits(Tq, Tk, Hq, Hkv, B);
+  const size_t q = dq > 1 ? sizeof(float) * (size_t)dq * (size_t)Tq * (size_t)Hq * (size_t)D : 0;
+  const size_t k = dkv > 1 ? 2 * sizeof(float) * (size_t)dkv * (size_t)Tk * (size_t)Hkv * (size_t)D : 0;
+  return backward_rows_bytes(Tq, Hq) + (q > k ? q : k);  // one after the other
 }
 
 nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, int64_t lddo_head, const void *q,
@@ -140,10 +149,10 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
   if ((st = check_device()) != NVFP4_OK) return st;
   const AttentionGradArgs g{{q, k, v, row_pitch(in[1], D), ldq_head, row_pitch(in[2], D), ldk_head, row_pitch(in[3], D), ldv_head, (int)Tq, (int)Tk, (int)Hq,
                              (int)(Hq / Hkv), (int)D, (int)B, cu_q, cu_k, (int)(Tq / B), (int)(Tk / B), causal != 0, scale,
-                             const_cast<void *>(out), ldo_token, ldo_head, const_cast<float *>(lse)},
+                             const_cast<void *>(out), ldo_token, ldo_head, const_cast<float *>(lse), attention_splits(Tq, Tk, Hq, B),
+                             reinterpret_cast<float *>(static_cast<char *>(workspace) + backward_rows_bytes(Tq, Hq))},
                             dout, row_pitch(in[0], D), lddo_head, dq, dk, dv, lddq_token, lddq_head, lddk_token, lddk_head,
-                            lddv_token, lddv_head, static_cast<float *>(workspace), attention_backward_splits(Tq, Tk, Hq, Hkv, B),
-                            reinterpret_cast<float *>(static_cast<char *>(workspace) + backward_rows_bytes(Tq, Hq))};
+                            lddv_token, lddv_head, static_cast<float *>(workspace), attention_backward_splits(Tq, Tk, Hq, Hkv, B)};
   return hip_status(launch_attention_backward(g, static_cast<hipStream_t>(stream)));
 }
 
