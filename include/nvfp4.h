@@ -534,7 +534,7 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
  * (T == B), else the tokens cu[b] .. cu[b + 1] - 1 are sequence b's last (device int32 [B + 1], ascending).
  * Tokens past the last sequence, and those whose position is negative or has no page, are not written.  MXFP8 is
  * bit-identical to nvfp4_mx8_quantize's rule.  Two tokens at one place (a page that two sequences write):
- * either one's values may remain.  T Hkv (D + 31) / 8 < 2^31.
+ * either one's values may remain.  (T + 15) Hkv (D + 31) / 8 < 2^31.
  *
  * nvfp4_paged_attention: out[b] = softmax(scale q[b] . keys) values over the lengths[b] tokens of sequence b
  * (q, out bf16 [B][Hq][D] at pitches; a sequence without tokens gets 0; out may be q itself with its pitches).  A

@@ -853,7 +853,7 @@ def _workspace(given, need: int, ref: torch.Tensor, dev: int):
     if given is None:
         if not need:
             return None, 0, 0
-        given = torch.empty(need, dtype=_u8, device=ref.device)
+        given = ref.new_empty(need, dtype=_u8)
         return given, given.data_ptr(), need
     if given.get_device() != dev or not given.is_contiguous():
         raise ValueError(f"workspace must be contiguous on cuda:{dev}, got one on {given.device}")
@@ -888,7 +888,7 @@ def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal
     p_v, vt, vh = _heads(v, "v", (Tk, Hkv, D), dev)
     p_cq, p_ck, batch = _offsets(cu_q, cu_k, batch, dev)
     if out is None:
-        out = torch.empty(shape, dtype=_bf16, device=q.device) if p_cq == 0 else torch.zeros(shape, dtype=_bf16, device=q.device)
+        out = q.new_empty(shape) if p_cq == 0 else q.new_zeros(shape)
         p_o, ot, oh = out.data_ptr(), Hq * D, D
     else:
         p_o, ot, oh = _heads(out, "out", shape, dev)
@@ -898,8 +898,7 @@ def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal
         p_l = _dense(lse, "lse", (Hq, Tq), _f32, dev)
         _written(lse, "lse")
     elif save_lse:
-        lse = torch.empty(Hq, Tq, dtype=_f32, device=q.device) if p_cq == 0 else \
-            torch.full((Hq, Tq), -math.inf, dtype=_f32, device=q.device)
+        lse = q.new_empty((Hq, Tq), dtype=_f32) if p_cq == 0 else q.new_full((Hq, Tq), -math.inf, dtype=_f32)
         p_l = lse.data_ptr()
     L = lib()
     workspace, p_w, n = _workspace(workspace, L.nvfp4_attention_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch), q, dev)
@@ -937,7 +936,7 @@ def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     grads = []
     for t, name, shape in ((dq, "dq", shape_q), (dk, "dk", shape_k), (dv, "dv", shape_k)):
         if t is None:
-            t = (torch.empty if p_cq == 0 else torch.zeros)(shape, dtype=_bf16, device=q.device)
+            t = q.new_empty(shape) if p_cq == 0 else q.new_zeros(shape)
         else:
             _heads(t, name, shape, dev)
             _written(t, name)
@@ -1005,21 +1004,25 @@ def _paged(cache, page_table, lengths, Hkv: int, D: int, dev: int):
     k, v, ks, vs = cache
     if k.dim() != 4 or page_table.dim() != 2:
         raise ValueError("the cache must be [pages, Hkv, page size, D] and page_table [sequences, pages]")
-    pages, _, size, _ = k.shape
-    shape = (pages, Hkv, size, D)
+    pages, _, size, _ = have = k.shape
     B, most = page_table.shape
-    if (ks is None) != (vs is None):
-        raise ValueError("k_scales and v_scales are given together")
     dtype, p_ks, p_vs = _bf16, 0, 0
-    if ks is not None:
+    if ks is not None or vs is not None:
+        if ks is None or vs is None:
+            raise ValueError("k_scales and v_scales are given together")
         dtype, groups = _u8, (pages, Hkv, size, (D + 31) // 32)
         p_ks, p_vs = _dense(ks, "k_scales", groups, _u8, dev), _dense(vs, "v_scales", groups, _u8, dev)
-    p_k, p_v = _dense(k, "the cache's k", shape, dtype, dev), _dense(v, "the cache's v", shape, dtype, dev)
-    _dense(lengths, "lengths", (B,), _i32, dev)
-    if page_table.dtype is not _i32 or page_table.get_device() != dev or (page_table.stride(1) != 1 and most > 1):
+    ld, step = page_table.stride()
+    if not (have == (pages, Hkv, size, D) and v.shape == have and k.dtype is dtype and v.dtype is dtype and k.is_contiguous()
+            and v.is_contiguous() and k.get_device() == dev and v.get_device() == dev and lengths.shape == (B,)
+            and lengths.dtype is _i32 and lengths.is_contiguous() and lengths.get_device() == dev
+            and page_table.dtype is _i32 and page_table.get_device() == dev and (step == 1 or most <= 1)):
+        _dense(k, "the cache's k", (pages, Hkv, size, D), dtype, dev)
+        _dense(v, "the cache's v", (pages, Hkv, size, D), dtype, dev)
+        _dense(lengths, "lengths", (B,), _i32, dev)
         raise ValueError(f"page_table must be int32 with unit stride along pages on cuda:{dev}, got {page_table.dtype} "
                          f"on {page_table.device}")
-    return p_k, p_ks, p_v, p_vs, pages, size, page_table.data_ptr(), page_table.stride(0) if B > 1 else most, most
+    return k.data_ptr(), p_ks, v.data_ptr(), p_vs, pages, size, page_table.data_ptr(), ld if B > 1 else most, most
 
 
 def nvfp4_cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
@@ -1072,7 +1075,7 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.
         raise ValueError(f"page_table has {page_table.shape[0]} sequences, q {B}")
     ck, cks, cv, cvs, pages, size, table, ld, most = _paged(cache, page_table, lengths, Hkv, D, dev)
     if out is None:
-        out = torch.empty(shape, dtype=_bf16, device=q.device)
+        out = q.new_empty(shape)
         p_o, ot, oh = out.data_ptr(), Hq * D, D
     else:
         p_o, ot, oh = _heads(out, "out", shape, dev)

@@ -165,7 +165,7 @@ nvfp4_status_t nvfp4_cache_append(const void *k, int64_t ldk_token, int64_t ldk_
   nvfp4_status_t st = check_cache(k_cache, k_scales, v_cache, v_scales, pages, page_size, page_table, ld_table, max_pages,
                                   lengths, B, Hkv, D);
   if (st != NVFP4_OK) return st;
-  if (T < 0 || (Hkv > 0 && T >= kThreads / (Hkv * ((D + 31) / 8))) || (!cu && T != B)) return NVFP4_ERR_SHAPE;
+  if (T < 0 || (Hkv > 0 && T + 15 >= kThreads / (Hkv * ((D + 31) / 8))) || (!cu && T != B)) return NVFP4_ERR_SHAPE;
   if (T == 0 || Hkv == 0 || B == 0) return NVFP4_OK;
   if ((st = check_heads({k, T, Hkv, ldk_token, ldk_head}, D, false)) != NVFP4_OK ||
       (st = check_heads({v, T, Hkv, ldv_token, ldv_head}, D, false)) != NVFP4_OK)

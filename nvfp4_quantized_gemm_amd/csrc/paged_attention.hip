@@ -11,39 +11,47 @@ namespace {
 
 // ---- append -------------------------------------------------------------------------------------------
 
-// A thread takes 8 values of a row (a token's head), of the key and of the value.  MX8: the 4 threads of a block of 32
-// find its scale together; blocks past D are zeros.
-template <bool MX8>
-__global__ __launch_bounds__(256) void k_cache_append(const CacheAppendArgs a) {
+// Row of the cache that a token's keys and values go to, or -1 where it has no place.
+__device__ __forceinline__ int64_t cache_row(const CacheAppendArgs &a, int t, int head) {
   const PagedCacheArgs &c = a.c;
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t row = fastdiv(i, a.per_row), piece = i - row * a.per_row.d;
-  const uint32_t t = fastdiv(row, a.heads), head = row - t * a.heads.d;
-  if (t >= (uint32_t)a.T) return;
-  const bool inside = piece < (uint32_t)c.D / 8;
-  u32x4 w[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-  if (inside) {  // on their way while the place is found
-    w[0] = load16<true>(static_cast<const uint16_t *>(a.k) + t * a.ldk_t + head * a.ldk_h + 8 * piece);
-    w[1] = load16<true>(static_cast<const uint16_t *>(a.v) + t * a.ldv_t + head * a.ldv_h + 8 * piece);
-  }
-  int b = (int)t;
+  int b = t;
   int64_t behind = 1;  // tokens of the sequence from this one on
   if (a.cu) {
     int lo = 0, hi = c.B;  // the last b with cu[b] <= t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= (int)t) lo = mid;
+      if (a.cu[mid] <= t) lo = mid;
       else hi = mid;
     }
     b = lo;
     behind = (int64_t)a.cu[b + 1] - t;
-    if (behind <= 0 || a.cu[b] > (int)t) return;
+    if (behind <= 0 || a.cu[b] > t) return -1;
   }
   const int64_t pos = c.lengths[b] - behind;
-  if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) return;
+  if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) return -1;
   const int page = c.table[b * c.ld_table + (pos >> c.page_shift)];
-  if (page < 0 || page >= c.pages) return;
-  const int64_t at = (((int64_t)page * c.Hkv + head) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+  if (page < 0 || page >= c.pages) return -1;
+  return (((int64_t)page * c.Hkv + head) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+}
+
+// A thread takes 8 values of a row (a token's head), of the key and of the value.  Rows go by 16 tokens of a head, which lie
+// side by side in the cache.  MX8: the 4 threads of a block of 32 find its scale together; blocks past D are zeros.
+// Three loads follow one another before a row's place is known: the values are on their way meanwhile.
+template <bool MX8>
+__global__ __launch_bounds__(256) void k_cache_append(const CacheAppendArgs a) {
+  const PagedCacheArgs &c = a.c;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t row = fastdiv(i, a.per_row), piece = i - row * a.per_row.d;
+  const uint32_t group = row >> 4, block = fastdiv(group, a.heads), head = group - block * a.heads.d, t = 16 * block + (row & 15);
+  if (t >= (uint32_t)a.T) return;
+  const bool inside = piece < (uint32_t)c.D / 8;
+  u32x4 w[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  if (inside) {
+    w[0] = load16<true>(static_cast<const uint16_t *>(a.k) + t * a.ldk_t + head * a.ldk_h + 8 * piece);
+    w[1] = load16<true>(static_cast<const uint16_t *>(a.v) + t * a.ldv_t + head * a.ldv_h + 8 * piece);
+  }
+  const int64_t at = cache_row(a, (int)t, (int)head);
+  if (at < 0) return;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     void *const to = j ? c.v : c.k;
@@ -449,7 +457,7 @@ hipError_t launch_cache_append(CacheAppendArgs a, hipStream_t stream) {
   const int per_row = a.c.ks ? (a.c.D + 31) / 32 * 4 : a.c.D / 8;
   a.per_row = make_fastdiv((uint32_t)per_row);
   a.heads = make_fastdiv((uint32_t)a.c.Hkv);
-  const int64_t threads = (int64_t)a.T * a.c.Hkv * per_row;  // below 2^31, the call checked
+  const int64_t threads = ((int64_t)a.T + 15) / 16 * 16 * a.c.Hkv * per_row;  // below 2^32, the call checked
   const dim3 grid((unsigned)((threads + 255) / 256));
   if (a.c.ks) k_cache_append<true><<<grid, dim3(256), 0, stream>>>(a);
   else k_cache_append<false><<<grid, dim3(256), 0, stream>>>(a);
@@ -458,12 +466,14 @@ hipError_t launch_cache_append(CacheAppendArgs a, hipStream_t stream) {
 
 // Workgroups for about 6 on each of 256 CUs (64 sequences of all lengths to 8192, MXFP8: 4 a CU 121 us, 8 116 us; two of
 // 131072, bf16: 134, 136), but none with less than a step of keys.
+// Short sequences are not split: a second launch costs what four steps take.
 int paged_attention_splits(int64_t B, int64_t Hq, int64_t Hkv, int64_t capacity) {
+  if (capacity <= 4 * kStep) return 1;
   const int64_t group = Hq / Hkv, blocks = B * Hkv * ((group + columns_of(group) - 1) / columns_of(group));
   int64_t n = (1536 + blocks - 1) / blocks;
   n = n < kMaxSplits ? n : kMaxSplits;
   const int64_t most = (capacity + kStep - 1) / kStep;
-  return (int)(n < most ? n : most > 1 ? most : 1);
+  return (int)(n < most ? n : most);
 }
 
 hipError_t launch_paged_attention(const PagedAttentionArgs &a, hipStream_t stream) {
