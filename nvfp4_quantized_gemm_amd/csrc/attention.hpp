@@ -8,6 +8,7 @@
 // operand of the next without a move between lanes, as long as its A operand lists k in the same order.
 #pragma once
 #include "launch.hpp"
+#include "sequence_index.hpp"
 
 namespace nvfp4 {
 
@@ -19,22 +20,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---- sequences ----------------------------------------------------------------------------------------
 
-// Rows of a sequence; whatever the offsets hold, inside [0, T).
-struct SeqRows {
-  int begin, n;
-};
-__device__ __forceinline__ SeqRows seq_rows(const int32_t *cu, int b, int T, int per) {
-  if (!cu) return {b * per, per};
-  const int lo = min(max(cu[b], 0), T), hi = min(max(cu[b + 1], lo), T);
-  return {lo, hi - lo};
-}
-
-// Blocks of BLK rows of packed sequences are numbered by slots: sequence b's begin at cu[b] / BLK + b, which
-// leaves it at least ceil(n / BLK) of them, so a block finds its sequence by a search, and nobody has to
-// know the lengths on the host.  (Equal sequences, cu == NULL: per / BLK rounded up for each.)
-inline int64_t attention_slots(int64_t T, int64_t B, bool packed, int blk) {
-  return packed ? T / blk + B : B * ((T / (B > 0 ? B : 1) + blk - 1) / blk);
-}
+// The sequence of a slot, and which of its blocks that is (none of them where blk is negative or past its end).
 template <int BLK>
 __device__ __forceinline__ void find_block(int slot, const int32_t *cu, int B, int T, int per, int lane, int &b, int &blk) {
   if (!cu) {
@@ -46,17 +32,14 @@ __device__ __forceinline__ void find_block(int slot, const int32_t *cu, int B, i
   int lo = 0, len = B;  // the last b with cu[b] / BLK + b <= slot: 64 candidates at a time
   while (len > 1) {
     const int step = (len + 63) >> 6, at = lane * step;
-    const bool here = at < len && min(max(cu[lo + min(at, len - 1)], 0), T) / BLK + lo + at <= slot;
+    const bool here = at < len && first_slot(cu, lo + min(at, len - 1), T, BLK) <= slot;
     const int n = max((int)__popcll(__ballot(here)), 1);
     lo += (n - 1) * step;
     len = min(step, len - (n - 1) * step);
   }
   b = __builtin_amdgcn_readfirstlane(lo);
-  blk = slot - (min(max(cu[b], 0), T) / BLK + b);
+  blk = slot - first_slot(cu, b, T, BLK);
 }
-
-// Rows of all sequences together.
-__device__ __forceinline__ int rows_in_use(const int32_t *cu, int B, int T) { return cu ? min(max(cu[B], 0), T) : T; }
 
 // Which block of which head: neighbouring workgroups lie on different XCDs, so where the heads divide evenly
 // each XCD takes its own, and all blocks that read a key head's rows share an L2.  slots_first: block by block

@@ -165,7 +165,7 @@ nvfp4_status_t nvfp4_cache_append(const void *k, int64_t ldk_token, int64_t ldk_
   nvfp4_status_t st = check_cache(k_cache, k_scales, v_cache, v_scales, pages, page_size, page_table, ld_table, max_pages,
                                   lengths, B, Hkv, D);
   if (st != NVFP4_OK) return st;
-  if (T < 0 || (Hkv > 0 && T + 15 >= kThreads / (Hkv * ((D + 31) / 8))) || (!cu && T != B)) return NVFP4_ERR_SHAPE;
+  if (T < 0 || (Hkv > 0 && T >= kThreads / (Hkv * ((D + 31) / 8)) - 15) || (!cu && T != B)) return NVFP4_ERR_SHAPE;
   if (T == 0 || Hkv == 0 || B == 0) return NVFP4_OK;
   if ((st = check_heads({k, T, Hkv, ldk_token, ldk_head}, D, false)) != NVFP4_OK ||
       (st = check_heads({v, T, Hkv, ldv_token, ldv_head}, D, false)) != NVFP4_OK)
@@ -188,7 +188,7 @@ nvfp4_status_t nvfp4_cache_append(const void *k, int64_t ldk_token, int64_t ldk_
 
 size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   if (B <= 0 || B >= (1 << 16) || Hq <= 0 || Hq > (1 << 16) || Hkv <= 0 || Hq % Hkv != 0 || D < 8 || D > kAttentionMaxD ||
-      capacity < 0 || capacity >= ((int64_t)1 << 31))
+      D % 8 != 0 || capacity < 0 || capacity >= ((int64_t)1 << 31))
     return 0;
   const int splits = paged_attention_splits(B, Hq, Hkv, capacity);
   return splits > 1 ? sizeof(float) * (size_t)B * (size_t)Hq * (size_t)splits * (size_t)(D + 2) : 0;

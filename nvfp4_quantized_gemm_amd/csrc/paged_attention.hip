@@ -11,29 +11,6 @@ namespace {
 
 // ---- append -------------------------------------------------------------------------------------------
 
-// Row of the cache that a token's keys and values go to, or -1 where it has no place.
-__device__ __forceinline__ int64_t cache_row(const CacheAppendArgs &a, int t, int head) {
-  const PagedCacheArgs &c = a.c;
-  int b = t;
-  int64_t behind = 1;  // tokens of the sequence from this one on
-  if (a.cu) {
-    int lo = 0, hi = c.B;  // the last b with cu[b] <= t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    behind = (int64_t)a.cu[b + 1] - t;
-    if (behind <= 0 || a.cu[b] > t) return -1;
-  }
-  const int64_t pos = c.lengths[b] - behind;
-  if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) return -1;
-  const int page = c.table[b * c.ld_table + (pos >> c.page_shift)];
-  if (page < 0 || page >= c.pages) return -1;
-  return (((int64_t)page * c.Hkv + head) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
-}
-
 // A thread takes 8 values of a row (a token's head), of the key and of the value.  Rows go by 16 tokens of a head, which lie
 // side by side in the cache.  MX8: the 4 threads of a block of 32 find its scale together; blocks past D are zeros.
 // Three loads follow one another before a row's place is known: the values are on their way meanwhile.
@@ -50,8 +27,10 @@ __global__ __launch_bounds__(256) void k_cache_append(const CacheAppendArgs a) {
     w[0] = load16<true>(static_cast<const uint16_t *>(a.k) + t * a.ldk_t + head * a.ldk_h + 8 * piece);
     w[1] = load16<true>(static_cast<const uint16_t *>(a.v) + t * a.ldv_t + head * a.ldv_h + 8 * piece);
   }
-  const int64_t at = cache_row(a, (int)t, (int)head);
-  if (at < 0) return;
+  const TokenPlace place = token_place(a.cu, c.lengths, c.B, (int)t);
+  const int page = page_of(c.table + place.b * c.ld_table, place.pos, c.page_shift, c.max_pages, c.pages);
+  if (page < 0) return;
+  const int64_t at = cache_row(page, (int)head, c.Hkv, place.pos, c.page_shift);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     void *const to = j ? c.v : c.k;
@@ -127,10 +106,6 @@ __device__ __forceinline__ int split_keys(int len, int splits) {
   const int steps = (len + kStep - 1) / kStep;
   return (steps + splits - 1) / splits * kStep;
 }
-__device__ __forceinline__ int tokens_of(const PagedCacheArgs &c, int b) {
-  return (int)min((int64_t)max(c.lengths[b], 0), (int64_t)c.max_pages << c.page_shift);
-}
-
 // What a lane brings of a tile, kN runs of W values (W = 8: 16 bytes of bf16, 8 of MXFP8; W = 16: 16 bytes of MXFP8,
 // half the loads, where D is whole 16 values and a half of the tile whole loads): offsets in the cache, from the first
 // row of their half, of the scales, and places in LDS.
@@ -203,12 +178,12 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x, kv = blockIdx.y % c.Hkv, first = blockIdx.y / c.Hkv * (16 * NC), b = blockIdx.z;
-  const int len = tokens_of(c, b), run = split_keys(len, a.splits), lo = split * run, hi = min(lo + run, len);
+  const int len = tokens_of(c.lengths[b], c.page_shift, c.max_pages), run = split_keys(len, a.splits), lo = split * run, hi = min(lo + run, len);
   if (lo >= len && split > 0) return;
   const int heads = min(a.group - first, 16 * NC);
 
   const int32_t *table = c.table + b * c.ld_table;
-  const int nb = (c.D + 31) / 32, mask = (1 << c.page_shift) - 1;
+  const int nb = (c.D + 31) / 32;
   uint8_t *const tile = smem + wave * kPart;
   Pieces<P, MX8, W> pieces;
   pieces.find(lane, c.D, nb);
@@ -222,10 +197,9 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int pos = key0 + 16 * half;
-      const int page = pos < hi ? __builtin_amdgcn_readfirstlane(table[pos >> c.page_shift]) : -1;
-      const bool ok = page >= 0 && page < c.pages;
-      w.at[half] = ok ? (((int64_t)page * c.Hkv + kv) << c.page_shift) + (pos & mask) : 0;
-      w.left[half] = ok ? min(hi - pos, 16) : 0;
+      const int page = pos < hi ? __builtin_amdgcn_readfirstlane(page_of(table, pos, c.page_shift, c.max_pages, c.pages)) : -1;
+      w.at[half] = page >= 0 ? cache_row(page, kv, c.Hkv, pos, c.page_shift) : 0;
+      w.left[half] = page >= 0 ? min(hi - pos, 16) : 0;
     }
     return w;
   };
@@ -382,7 +356,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
 __global__ __launch_bounds__(256) void k_paged_join(const PagedAttentionArgs a) {
   const PagedCacheArgs &c = a.c;
   const int head = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int len = tokens_of(c, b), run = split_keys(len, a.splits), n = run > 0 ? (len + run - 1) / run : 0;
+  const int len = tokens_of(c.lengths[b], c.page_shift, c.max_pages), run = split_keys(len, a.splits), n = run > 0 ? (len + run - 1) / run : 0;
   const int64_t who = (int64_t)b * a.Hq + head;
   const float *const part = a.partial + who * a.splits * c.D;
   const float *const st = a.partial + (int64_t)c.B * a.Hq * a.splits * c.D + 2 * who * a.splits;
