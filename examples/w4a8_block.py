@@ -1,13 +1,16 @@
 """The attention half of a transformer block on the 8-bit activation path, as a video or image model runs it:
 
   serving   residual + RMS norm -> MXFP8 -> QKV product with an MXFP4 weight -> rotary positions of time, height and
-            width on q and k, in place in the QKV output -> attention (torch, fp32) -> MXFP8 -> output projection ->
-            the next norm with the residual's addition
+            width on q and k, in place in the QKV output -> attention (torch in fp32, or the library's on q, k and v
+            where they lie) -> MXFP8 -> output projection -> the next norm with the residual's addition
+  decoding  the same block in a causal model: prompts of different lengths packed together, their keys and values into
+            a paged MXFP8 cache, then one token per sequence and step over that cache
   training  the same block with bf16 weights in quantization-aware training: what serving rounds is rounded to the
             same values (MXFP8 inputs of both products, MXFP4 weights), straight-through gradients, a few steps of
             gradient descent
 
-  python examples/w4a8_block.py [--grid 4,32,32] [--heads 16] [--head-dim 72] [--steps 3]
+  python examples/w4a8_block.py [--grid 4,32,32] [--heads 16] [--head-dim 72] [--steps 3] [--attention torch|library]
+                                [--prompts 300,17,1000] [--tokens 8]
 """
 import argparse
 import os
@@ -33,26 +36,61 @@ def attention(q, k, v):
     return out[0].transpose(0, 1).reshape(q.shape[1], -1)
 
 
+def library_attention(q, k, v):
+    """The same on the library's kernels, bf16: no copies, differentiable."""
+    return nv.attention(q, k, v).flatten(1)
+
+
 class ServingBlock:
     """MXFP4 weights, MXFP8 activations."""
 
-    def __init__(self, hidden: int, heads: int, axis_dims, w_qkv, w_out, norm_weight, next_norm_weight):
+    def __init__(self, hidden: int, heads: int, axis_dims, w_qkv, w_out, norm_weight, next_norm_weight, attend=attention):
+        self.attend = attend
         self.heads, self.head_dim, self.axis_dims = heads, hidden // heads, axis_dims
         self.qkv, self.out = nv.nvfp4_mx_quantize(w_qkv), nv.nvfp4_mx_quantize(w_out)  # once per weight
         self.norm_weight, self.next_norm_weight = norm_weight, next_norm_weight
         self.inv_freq = nv.rope_inv_freq(axis_dims, device=w_qkv.device)
 
-    def __call__(self, x, residual, positions):
-        """x, residual [T, hidden] bf16 -> (the next linear's MXFP8 codes and scales, the residual stream)."""
-        T, hidden = x.shape
+    def before(self, x, residual, positions):
+        """(q, k, v [T, heads, head_dim] as views of the QKV output, q and k turned; the residual stream)."""
         n = nv.nvfp4_rmsnorm(x, residual, self.norm_weight)
-        qkv = nv.nvfp4_mx_gemm_w4a8(n.codes, n.scales, *self.qkv).view(T, 3 * self.heads, self.head_dim)
+        qkv = nv.nvfp4_mx_gemm_w4a8(n.codes, n.scales, *self.qkv).view(x.shape[0], 3 * self.heads, self.head_dim)
         qk = qkv[:, : 2 * self.heads]
         nv.nvfp4_rope_axes(qk, positions, self.axis_dims, self.inv_freq, out=qk)
-        att = attention(*qkv.split(self.heads, 1))
+        return qkv.split(self.heads, 1), n.h
+
+    def after(self, att, h):
         y = nv.nvfp4_mx_gemm_w4a8(*nv.nvfp4_mx8_quantize(att), *self.out)
-        after = nv.nvfp4_rmsnorm(y, n.h, self.next_norm_weight, h=n.h)
+        after = nv.nvfp4_rmsnorm(y, h, self.next_norm_weight, h=h)
         return after.codes, after.scales, after.h
+
+    def __call__(self, x, residual, positions):
+        """x, residual [T, hidden] bf16 -> (the next linear's MXFP8 codes and scales, the residual stream)."""
+        qkv, h = self.before(x, residual, positions)
+        return self.after(self.attend(*qkv), h)
+
+    def prompts(self, x, residual, positions, cu, cache, page_table, lengths):
+        """The same, causal, for the packed prompts that cu names; their keys and values go into the cache."""
+        (q, k, v), h = self.before(x, residual, positions)
+        nv.nvfp4_cache_append(k, v, cache, page_table, lengths, cu)
+        return self.after(nv.nvfp4_attention(q, k, v, causal=True, cu_q=cu, cu_k=cu)[0].flatten(1), h)
+
+    def tokens(self, x, residual, positions, cache, page_table, lengths):
+        """The same for one new token of each sequence, which lengths counts already."""
+        (q, k, v), h = self.before(x, residual, positions)
+        nv.nvfp4_cache_append(k, v, cache, page_table, lengths)
+        return self.after(nv.nvfp4_paged_attention(q, cache, page_table, lengths).flatten(1), h)
+
+
+def sequence_pages(tokens, page_size: int, device):
+    """(pages of a cache, page table) for sequences of up to so many tokens each."""
+    need = [-(-n // page_size) for n in tokens]
+    table = torch.full((len(need), max(need)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    return at, table.to(device)
 
 
 class StraightThrough(torch.autograd.Function):
@@ -81,14 +119,14 @@ def mx8_activation(t, dtype):
     return StraightThrough.apply(t, values.view(t.shape).to(dtype))
 
 
-def training_block(x, residual, positions, axis_dims, inv_freq, heads, w_qkv, w_out, norm_weight):
+def training_block(x, residual, positions, axis_dims, inv_freq, heads, w_qkv, w_out, norm_weight, attend=attention):
     """The block for quantization-aware training: (output, residual stream), differentiable."""
     T, hidden = x.shape
     y, h = nv.rmsnorm(x, residual, norm_weight, fake_quantize=True)
     qkv = F.linear(y, mx4_weight(w_qkv)).view(T, 3 * heads, hidden // heads)
     q, k, v = qkv.split(heads, 1)
     q, k = (nv.rope_axes(t, positions, axis_dims, inv_freq) for t in (q, k))
-    return F.linear(mx8_activation(attention(q, k, v), x.dtype), mx4_weight(w_out)), h
+    return F.linear(mx8_activation(attend(q, k, v), x.dtype), mx4_weight(w_out)), h
 
 
 def make_inputs(tokens: int, hidden: int, device="cuda", seed: int = 0):
@@ -106,7 +144,11 @@ def main():
     ap.add_argument("--heads", type=int, default=16)
     ap.add_argument("--head-dim", type=int, default=72)
     ap.add_argument("--steps", type=int, default=3)
+    ap.add_argument("--attention", choices=("torch", "library"), default="torch")
+    ap.add_argument("--prompts", default="", help="lengths of packed prompts, to decode from")
+    ap.add_argument("--tokens", type=int, default=8, help="tokens to decode after each prompt")
     a = ap.parse_args()
+    attend = library_attention if a.attention == "library" else attention
     grid = [int(n) for n in a.grid.split(",")]
     hidden, tokens = a.heads * a.head_dim, grid[0] * grid[1] * grid[2]
     third = a.head_dim // 6 * 2
@@ -114,11 +156,28 @@ def main():
     x, residual, w_qkv, w_out, nw, nw2 = make_inputs(tokens, hidden)
     positions = grid_positions(*grid, x.device)
 
-    block = ServingBlock(hidden, a.heads, axis_dims, w_qkv, w_out, nw, nw2)
+    block = ServingBlock(hidden, a.heads, axis_dims, w_qkv, w_out, nw, nw2, attend)
     codes, scales, h = block(x, residual, positions)
     torch.cuda.synchronize()
     print(f"serving: {tokens} tokens, hidden {hidden}: codes {tuple(codes.shape)}, scales {tuple(scales.shape)}, "
           f"residual rms {h.float().square().mean().sqrt().item():.4f}")
+
+    if a.prompts:
+        lens = [int(n) for n in a.prompts.split(",")]
+        pages, table = sequence_pages([n + a.tokens for n in lens], 16, x.device)
+        cache = nv.paged_cache(pages, 16, a.heads, a.head_dim, mx8=True)
+        lengths = torch.tensor(lens, dtype=torch.int32, device=x.device)
+        cu = torch.tensor([0] + lens, device=x.device).cumsum(0).int()
+        place = lambda t: torch.stack([t, 0 * t, 0 * t], 1).float()  # noqa: E731
+        p = make_inputs(sum(lens), hidden, seed=1)
+        block.prompts(p[0], p[1], place(torch.cat([torch.arange(n, device=x.device) for n in lens])), cu, cache, table, lengths)
+        for step in range(a.tokens):
+            t = make_inputs(len(lens), hidden, seed=2 + step)
+            lengths += 1
+            _, _, h = block.tokens(t[0], t[1], place(lengths - 1), cache, table, lengths)
+        torch.cuda.synchronize()
+        print(f"decoding: {len(lens)} prompts, {a.tokens} tokens each, lengths {lengths.tolist()}, residual rms "
+              f"{h.float().square().mean().sqrt().item():.4f}")
 
     params = [t.clone().requires_grad_() for t in (w_qkv, w_out, nw)]
     target = 0.1 * torch.randn_like(x)
@@ -126,7 +185,7 @@ def main():
     optimizer = torch.optim.Adam(params, lr=1e-3)
     for step in range(a.steps):
         optimizer.zero_grad()
-        out, _ = training_block(x, residual, positions, axis_dims, inv_freq, a.heads, *params)
+        out, _ = training_block(x, residual, positions, axis_dims, inv_freq, a.heads, *params, attend)
         loss = (out.float() - target.float()).square().mean()
         loss.backward()
         optimizer.step()
