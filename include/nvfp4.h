@@ -481,7 +481,8 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
  *   workspace    nvfp4_attention_workspace_bytes bytes (0 but where there are few queries, whose keys several
  *                workgroups then share, joined in a fixed order), 16-byte aligned, no initialization.
  * Equal inputs give equal bits.  Scores, exponentials and sums are fp32; the exponentials are rounded to bf16 for their product with v.
- * Infinities and NaN reach only the queries that attend them.  Tq == 0, Hq == 0 or B == 0 is valid and
+ * Infinities and NaN reach only the queries that attend them; debug checks scan nothing for the calls from here
+ * on, which have no preconditions on device data.  Tq == 0, Hq == 0 or B == 0 is valid and
  * touches nothing; Tk == 0 writes zeros.
  * ------------------------------------------------------------------------------------------- */
 size_t nvfp4_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, int64_t B);

