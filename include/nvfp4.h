@@ -470,7 +470,7 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
  *                h / (Hq / Hkv).
  *   D            8 .. 128, D % 8 == 0.   Token pitches D .. 2^23 - 1; Hq (max(Tq, Tk) / 32 + B + 1) < 2^23,
                 Hq <= 2^16, B <= 2^20.
- *   cu_q, cu_k   both NULL: B sequences of Tq / B queries and Tk / B keys (whole numbers).  Else device
+ *   cu_q, cu_k   both NULL: B >= 1 sequences of Tq / B queries and Tk / B keys (whole numbers).  Else device
  *                int32 [B + 1] (they may be one array): sequence b has the rows cu[b] .. cu[b + 1] - 1, in
  *                order, of any lengths (0 too).  Rows past the last sequence are not read, and of out and
  *                lse left as they were.  Offsets are taken into [0, T], so no content makes a call read or
@@ -527,7 +527,7 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
  *                       sequence b is row p % page_size of page page_table[b][p / page_size].  An entry
  *                       outside [0, pages) holds no tokens: nothing is read or written there.
  *   lengths             device int32 [B]: tokens of each sequence, taken into [0, max_pages page_size].
- *   max_pages page_size < 2^31, B Hkv and B Hq < 2^31, B < 2^16, Hq <= 2^16 with Hq a multiple of Hkv.
+ *   max_pages page_size < 2^30, B < 2^16, Hq <= 2^16 with Hq a multiple of Hkv.
  * No content of page_table, lengths or cu makes a call read or write outside its arrays.
  *
  * nvfp4_cache_append writes the keys and values k, v (bf16 [T][Hkv][D] at pitches, as for nvfp4_attention)

@@ -274,6 +274,7 @@ __global__ __launch_bounds__(64 * KW * RS) __attribute__((amdgpu_waves_per_eu(2,
     return again;
   };
   if (__syncthreads_or(pass(false))) pass(true);
+  if constexpr (VL) wait_vmem();  // the values', where there was no step to wait for them
   if constexpr (RS == 2) {
     f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + kw * (DB * 4 * 64) + lane;
     auto join = [&](f32x16(&x)[DB]) __attribute__((always_inline)) {

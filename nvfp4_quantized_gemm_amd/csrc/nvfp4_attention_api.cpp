@@ -11,6 +11,7 @@ using namespace nvfp4;
 
 namespace {
 
+constexpr int64_t kMaxCapacity = (int64_t)1 << 30;  // a sequence's positions, and a step past them, fit 32 bits
 constexpr int64_t kMaxPitch = (int64_t)1 << 23;  // offsets inside a tile of 64 rows fit 31 bits
 
 struct Heads {  // [T][H][D] bf16 at token and head pitches
@@ -39,7 +40,7 @@ nvfp4_status_t check_attention_shape(int64_t Tq, int64_t Tk, int64_t Hq, int64_t
       D > kAttentionMaxD || D % 8 != 0 || B < 0 || B > (1 << 20) || (Hq > 0 && (Hkv == 0 || Hq % Hkv != 0)))
     return NVFP4_ERR_SHAPE;
   if ((cu_q == nullptr) != (cu_k == nullptr)) return NVFP4_ERR_NULL;
-  if (!cu_q && B > 0 && (Tq % B != 0 || Tk % B != 0)) return NVFP4_ERR_SHAPE;
+  if (!cu_q && (B > 0 ? Tq % B != 0 || Tk % B != 0 : Tq > 0 || Tk > 0)) return NVFP4_ERR_SHAPE;
   // at most a workgroup of 512 threads per head and 32 rows, and 2^32 threads
   if (((Tq > Tk ? Tq : Tk) / 32 + B + 1) * Hq >= ((int64_t)1 << 23)) return NVFP4_ERR_SHAPE;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return NVFP4_ERR_MODE;
@@ -58,7 +59,7 @@ nvfp4_status_t check_cache(const void *k, const uint8_t *ks, const void *v, cons
   constexpr int64_t kInt = (int64_t)1 << 31;
   if (D < 8 || D > kAttentionMaxD || D % 8 != 0 || Hkv < 0 || Hkv > (1 << 16) || B < 0 || B >= (1 << 16) || pages < 0 ||
       pages >= kInt || page_size < 16 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0 || max_pages < 0 ||
-      max_pages >= kInt / page_size || (Hkv > 0 && pages > kMaxElems / (Hkv * page_size * D)))
+      max_pages >= kMaxCapacity / page_size || (Hkv > 0 && pages > kMaxElems / (Hkv * page_size * D)))
     return NVFP4_ERR_SHAPE;
   if ((ks == nullptr) != (vs == nullptr)) return NVFP4_ERR_NULL;
   if (B == 0 || Hkv == 0) return NVFP4_OK;
@@ -188,7 +189,7 @@ nvfp4_status_t nvfp4_cache_append(const void *k, int64_t ldk_token, int64_t ldk_
 
 size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   if (B <= 0 || B >= (1 << 16) || Hq <= 0 || Hq > (1 << 16) || Hkv <= 0 || Hq % Hkv != 0 || D < 8 || D > kAttentionMaxD ||
-      D % 8 != 0 || capacity < 0 || capacity >= ((int64_t)1 << 31))
+      D % 8 != 0 || capacity < 0 || capacity >= kMaxCapacity)
     return 0;
   const int splits = paged_attention_splits(B, Hq, Hkv, capacity);
   return splits > 1 ? sizeof(float) * (size_t)B * (size_t)Hq * (size_t)splits * (size_t)(D + 2) : 0;

@@ -39,6 +39,7 @@ def test_shapes_and_scale(L, call):
         assert call(L, **kw) == S.ERR_SHAPE, kw
     for kw in (dict(B=3, Tq=100, Tk=90), dict(B=3, Tq=99, Tk=91)):  # equal sequences
         assert call(L, cq=None, ck=None, **kw) == S.ERR_SHAPE, kw
+    assert call(L, cq=None, ck=None, B=0) == S.ERR_SHAPE  # rows of no sequence
     for scale in (0.0, -1.0, float("nan"), float("inf")):
         assert call(L, scale=scale) == S.ERR_MODE, scale
     assert call(L, cq=None) == S.ERR_NULL and call(L, ck=None) == S.ERR_NULL
@@ -76,7 +77,7 @@ def test_workspaces(L):
     n = L.nvfp4_paged_attention_workspace_bytes(2, 32, 8, 128, 8192)
     assert n > 0 and L.nvfp4_paged_attention_workspace_bytes(2, 32, 8, 128, 128) == 0
     for args in ((0, 32, 8, 128, 8192), (1 << 16, 32, 8, 128, 8192), (2, 30, 8, 128, 8192), (2, 32, 0, 128, 8192), (2, 32, 8, 12, 8192),
-                 (2, 32, 8, 128, -1), (2, 32, 8, 128, 1 << 31)):
+                 (2, 32, 8, 128, -1), (2, 32, 8, 128, 1 << 30)):
         assert L.nvfp4_paged_attention_workspace_bytes(*args) == 0, args
 
 
@@ -115,7 +116,7 @@ def paged(L, q=P[0], qt=256, qh=64, B=4, Hq=4, H=2, D=64, ck=P[4], ks=P[5], cv=P
 @pytest.mark.parametrize("call", [append, paged])
 def test_caches(L, call):
     for kw in (dict(D=0), dict(D=12), dict(D=136), dict(H=-1), dict(B=-1), dict(B=1 << 16), dict(pages=-1), dict(pages=1 << 31),
-               dict(size=0), dict(size=8), dict(size=24), dict(size=1 << 21), dict(most=-1), dict(most=1 << 28), dict(pages=1 << 30, size=1 << 14)):
+               dict(size=0), dict(size=8), dict(size=24), dict(size=1 << 21), dict(most=-1), dict(most=1 << 28), dict(most=1 << 26, ld=1 << 26), dict(pages=1 << 30, size=1 << 14)):
         assert call(L, **kw) == S.ERR_SHAPE, kw
     for name in ("ck", "ks", "cv", "vs", "table", "le"):
         assert call(L, **{name: None}) == S.ERR_NULL, name
