@@ -469,7 +469,7 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
  *   k, v         bf16 [Tk][Hkv][D], the same; Hq a multiple of Hkv, query head h reads key head
  *                h / (Hq / Hkv).
  *   D            8 .. 128, D % 8 == 0.   Token pitches D .. 2^23 - 1; Hq (max(Tq, Tk) / 32 + B + 1) < 2^23,
-                Hq <= 2^16, B <= 2^20.
+ *                Hq <= 2^16, B <= 2^20.
  *   cu_q, cu_k   both NULL: B >= 1 sequences of Tq / B queries and Tk / B keys (whole numbers).  Else device
  *                int32 [B + 1] (they may be one array): sequence b has the rows cu[b] .. cu[b + 1] - 1, in
  *                order, of any lengths (0 too).  Rows past the last sequence are not read, and of out and

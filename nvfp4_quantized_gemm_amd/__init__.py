@@ -903,7 +903,7 @@ def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal
     L = lib()
     workspace, p_w, n = _workspace(workspace, L.nvfp4_attention_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch), q, dev)
     st = L.nvfp4_attention(p_q, qt, qh, p_k, kt, kh, p_v, vt, vh, Tq, Tk, Hq, Hkv, D, p_cq, p_ck, batch, 1 if causal else 0,
-                           D ** -0.5 if scale is None else scale, p_o, ot, oh, p_l, p_w, n, _current_stream(dev))
+                           max(D, 1) ** -0.5 if scale is None else scale, p_o, ot, oh, p_l, p_w, n, _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_attention")
     return out, lse
@@ -944,7 +944,7 @@ def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     L = lib()
     workspace, p_w, n = _workspace(workspace, L.nvfp4_attention_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch), q, dev)
     st = L.nvfp4_attention_backward(*args, Tq, Tk, Hq, Hkv, D, p_cq, p_ck, batch, 1 if causal else 0,
-                                    D ** -0.5 if scale is None else scale, *_heads(grads[0], "dq", shape_q, dev),
+                                    max(D, 1) ** -0.5 if scale is None else scale, *_heads(grads[0], "dq", shape_q, dev),
                                     *_heads(grads[1], "dk", shape_k, dev), *_heads(grads[2], "dv", shape_k, dev),
                                     p_w, n, _current_stream(dev))
     if st:
@@ -1083,7 +1083,7 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.
     L = lib()
     workspace, p_w, n = _workspace(workspace, L.nvfp4_paged_attention_workspace_bytes(B, Hq, Hkv, D, most * size), q, dev)
     st = L.nvfp4_paged_attention(p_q, qt, qh, B, Hq, Hkv, D, ck, cks, cv, cvs, pages, size, table, ld, most,
-                                 lengths.data_ptr(), D ** -0.5 if scale is None else scale, p_o, ot, oh, p_w, n,
+                                 lengths.data_ptr(), max(D, 1) ** -0.5 if scale is None else scale, p_o, ot, oh, p_w, n,
                                  _current_stream(dev))
     if st:
         raise NVFP4Error(st, "nvfp4_paged_attention")

@@ -172,3 +172,17 @@ def test_long_prompt_prefix_of_shared_pages():
     n = torch.tensor([64, 64], dtype=torch.int32, device=DEV)
     out = nv.nvfp4_paged_attention(q, cache, both, n)
     assert torch.equal(out[0], out[1])
+
+
+def test_heads_of_no_size_are_refused_by_the_calls():
+    q, k, v, u, cu = call(SHAPES[0])
+    out, lse = nv.nvfp4_attention(q, k, v, save_lse=True, **cu)
+    none = lambda t: t[..., :0].contiguous()  # noqa: E731
+    with pytest.raises(nv.NVFP4Error):
+        nv.nvfp4_attention(none(q), none(k), none(v), **cu)
+    with pytest.raises(nv.NVFP4Error):
+        nv.nvfp4_attention_backward(none(u), none(q), none(k), none(v), none(out), lse, **cu)
+    cache = nv.paged_cache(4, 16, 2, 0)
+    table, lengths = torch.zeros(1, 4, dtype=torch.int32, device=DEV), torch.ones(1, dtype=torch.int32, device=DEV)
+    with pytest.raises(nv.NVFP4Error):
+        nv.nvfp4_paged_attention(none(q[:1]), cache, table, lengths)
