@@ -472,9 +472,11 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
  *                Hq <= 2^16, B <= 2^20.
  *   cu_q, cu_k   both NULL: B >= 1 sequences of Tq / B queries and Tk / B keys (whole numbers).  Else device
  *                int32 [B + 1] (they may be one array): sequence b has the rows cu[b] .. cu[b + 1] - 1, in
- *                order, of any lengths (0 too).  Rows past the last sequence are not read, and of out and
- *                lse left as they were.  Offsets are taken into [0, T], so no content makes a call read or
- *                write outside its arrays.
+ *                order, of any lengths (0 too).  Rows of no sequence, before cu[0] and from cu[B] on, are not
+ *                read, and of out and lse left as they were: cu + b of a longer array names some of a packed
+ *                batch's sequences.  Offsets have to ascend.  They are taken into [0, T], so no content
+ *                makes a call read or write outside its arrays; where they descend, what the rows between the
+ *                least and the largest get is not specified.
  *   scale        finite, > 0 (else NVFP4_ERR_MODE).
  *   out          may be q itself (same pitches), and otherwise must not overlap an input.
  *   lse          NULL, or fp32 [Hq][Tq] (the backward pass reads it).
@@ -499,7 +501,7 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
  * products; the sums are fp32 and run in a fixed order: equal inputs give equal bits.
  *   dout, out, dq   bf16 [Tq][Hq][D], dk, dv bf16 [Tk][Hkv][D], at their own pitches as above.
  *   dq, dk, dv      written; at no input's address (NVFP4_ERR_STRIDE) and not overlapping any array.  Rows
- *                   past the last sequence are left as they were; keys that nothing attends get 0.
+ *                   of no sequence are left as they were; keys that nothing attends get 0.
  *   workspace       nvfp4_attention_backward_workspace_bytes bytes, 16-byte aligned, no initialization (where there
  *                   are few queries or keys, several workgroups share a gradient and add it at the end).
  * B == 0 or Hq == 0 is valid and touches nothing; Tq == 0 writes dk = dv = 0. */

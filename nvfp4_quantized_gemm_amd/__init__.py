@@ -871,9 +871,10 @@ def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal
     of a QKV output are read in place).  Hq is a multiple of Hkv.  Returns (out, lse): out bf16 [Tq, Hq, D], lse fp32 [Hq, Tq], the
     log sums of exponentials that the backward pass reads (None without save_lse or a given lse).
 
-    cu_q, cu_k: int32 offsets [sequences + 1] of packed sequences; without them the rows are `batch` sequences of equal
-    length.  causal: query i of n_q attends keys up to i + n_k - n_q.  scale: D ** -0.5 by default.  Queries without keys
-    get 0 and -inf; so do, in new tensors, rows past the last sequence, which in given ones are left as they were."""
+    cu_q, cu_k: int32 offsets [sequences + 1] of packed sequences, ascending (the first may be above 0); without them the
+    rows are `batch` sequences of equal length.  causal: query i of n_q attends keys up to i + n_k - n_q.  scale: D ** -0.5
+    by default.  Queries without keys get 0 and -inf; so do, in new tensors, rows of no sequence, before the first and past
+    the last one, which in given ones are left as they were."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return nvfp4_attention(q, k, v, causal=causal, scale=scale, cu_q=cu_q, cu_k=cu_k, batch=batch,
@@ -918,7 +919,7 @@ def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
                              cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, batch: int = 1,
                              dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Gradients of nvfp4_attention from dout (the gradient of out), its inputs, its out and its lse, with the same
-    sequences, causal and scale.  Returns (dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]), bf16; rows past the last sequence are 0 in
+    sequences, causal and scale.  Returns (dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]), bf16; rows of no sequence are 0 in
     new tensors and left as they were in given ones (any strides as for q; not an input's memory)."""
     if stream is not None:
         with torch.cuda.stream(stream):

@@ -162,10 +162,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 }
 
 // Joins the splits in order: a thread has 4 values of a query's head.
-__global__ __launch_bounds__(256) void k_attention_join(const AttentionArgs a, const FastDiv per_row, const FastDiv heads) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x, r = fastdiv(i, per_row), d = 4 * (i - r * per_row.d);
+__global__ __launch_bounds__(kJoinThreads) void k_attention_join(const AttentionArgs a, const FastDiv per_row, const FastDiv heads) {
+  const uint32_t i = blockIdx.x * (uint32_t)kJoinThreads + threadIdx.x, r = fastdiv(i, per_row), d = 4 * (i - r * per_row.d);
   const uint32_t t = fastdiv(r, heads), head = r - t * heads.d;
-  if (t >= (uint32_t)rows_in_use(a.cu_q, a.B, a.Tq)) return;
+  if (!holds(joined_rows(a.cu_q, a.B, a.Tq), t)) return;
   const int64_t each = (int64_t)a.Tq * a.Hq;
   const f32x2 *const st = reinterpret_cast<const f32x2 *>(a.parts + a.splits * each * a.D) + r;
   float top = -INFINITY, total = 0.0f;
@@ -199,8 +199,8 @@ hipError_t launch(AttentionArgs a, hipStream_t stream) {
   k_attention<KS, DB, kWaves><<<dim3((unsigned)(a.slots * a.Hq * a.splits)), dim3(64 * kWaves), kLds, stream>>>(a);
   if (a.splits > 1) {
     const int64_t threads = (int64_t)a.Tq * a.Hq * (a.D / 4);  // few: the splits are for small problems
-    k_attention_join<<<dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream>>>(a, make_fastdiv((uint32_t)(a.D / 4)),
-                                                                                      make_fastdiv((uint32_t)a.Hq));
+    k_attention_join<<<dim3((unsigned)((threads + kJoinThreads - 1) / kJoinThreads)), dim3(kJoinThreads), 0, stream>>>(
+        a, make_fastdiv((uint32_t)(a.D / 4)), make_fastdiv((uint32_t)a.Hq));
   }
   return hipGetLastError();
 }

@@ -41,6 +41,21 @@ __device__ __forceinline__ void find_block(int slot, const int32_t *cu, int B, i
   blk = slot - first_slot(cu, b, T, BLK);
 }
 
+// Rows that sequences hold, for a kernel of kJoinThreads threads that joins what several workgroups summed: no row else was
+// computed, and the workspace holds anything there.  None where the offsets descend: which rows have blocks is not known
+// then.  (Calls whose sums are joined have at most 512 sequences, see attention_splits and attention_backward_splits.)
+constexpr int kJoinThreads = 256;
+__device__ __forceinline__ SeqRows joined_rows(const int32_t *cu, int B, int T) {
+  if (cu) {
+    bool down = false;
+    for (int b = threadIdx.x; b < B; b += kJoinThreads) down |= descends(cu, b, T);
+    if (__syncthreads_or(down)) return {0, 0};
+  }
+  const int begin = rows_before(cu, T);
+  return {begin, rows_in_use(cu, B, T) - begin};
+}
+__device__ __forceinline__ bool holds(const SeqRows &s, uint32_t row) { return row - (uint32_t)s.begin < (uint32_t)s.n; }
+
 // Which block of which head: neighbouring workgroups lie on different XCDs, so where the heads divide evenly
 // each XCD takes its own, and all blocks that read a key head's rows share an L2.  slots_first: block by block
 // over the heads (causal blocks with many tiles go first), else head by head.

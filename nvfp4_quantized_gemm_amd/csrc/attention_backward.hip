@@ -324,10 +324,10 @@ struct GradJoin {
   int64_t ld_t[2], ld_h[2];
   FastDiv per_row, heads;
 };
-__global__ __launch_bounds__(256) void k_gradient_join(const GradJoin g) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x, j = blockIdx.y;
+__global__ __launch_bounds__(kJoinThreads) void k_gradient_join(const GradJoin g) {
+  const uint32_t i = blockIdx.x * (uint32_t)kJoinThreads + threadIdx.x, j = blockIdx.y;
   const uint32_t r = fastdiv(i, g.per_row), at = 4 * (i - r * g.per_row.d), t = fastdiv(r, g.heads), head = r - t * g.heads.d;
-  if (t >= (uint32_t)rows_in_use(g.cu, g.B, g.T)) return;
+  if (!holds(joined_rows(g.cu, g.B, g.T), t)) return;
   const int64_t each = (int64_t)g.T * g.heads.d * g.D;
   const float *from = g.parts + j * each + (int64_t)r * g.D + at;
   f32x4 sum = {0, 0, 0, 0};
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(256) void k_gradient_join(const GradJoin g) {
 }
 void join(const GradJoin &g, int outputs, hipStream_t stream) {
   const int64_t threads = (int64_t)g.T * g.heads.d * (g.D / 4);  // few: the splits are for small problems
-  k_gradient_join<<<dim3((unsigned)((threads + 255) / 256), (unsigned)outputs), dim3(256), 0, stream>>>(g);
+  k_gradient_join<<<dim3((unsigned)((threads + kJoinThreads - 1) / kJoinThreads), (unsigned)outputs), dim3(kJoinThreads), 0, stream>>>(g);
 }
 
 constexpr int kKeyWaves = 4;

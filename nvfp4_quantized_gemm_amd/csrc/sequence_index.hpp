@@ -22,8 +22,12 @@ NVFP4_HOST_DEVICE SeqRows seq_rows(const int32_t *cu, int b, int T, int per) {
   const int lo = clamp_row(cu[b], T), hi = clamp_row(cu[b + 1], T);
   return {lo, hi > lo ? hi - lo : 0};
 }
-// Rows of all sequences together.
+// Rows before the first sequence, and up to the last one's end: where the offsets ascend, the sequences hold the rows
+// between, each row once, and blocks find every one.
+NVFP4_HOST_DEVICE int rows_before(const int32_t *cu, int T) { return cu ? clamp_row(cu[0], T) : 0; }
 NVFP4_HOST_DEVICE int rows_in_use(const int32_t *cu, int B, int T) { return cu ? clamp_row(cu[B], T) : T; }
+// Whether they descend at sequence b.
+NVFP4_HOST_DEVICE bool descends(const int32_t *cu, int b, int T) { return clamp_row(cu[b], T) > clamp_row(cu[b + 1], T); }
 
 // Blocks of blk rows of packed sequences are numbered by slots: sequence b's begin at cu[b] / blk + b, which
 // leaves it at least ceil(n / blk) of them, so a block finds its sequence by a search, and nobody has to
