@@ -483,7 +483,8 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
  *   workspace    nvfp4_attention_workspace_bytes bytes (0 but where there are few queries, whose keys several
  *                workgroups then share, joined in a fixed order), 16-byte aligned, no initialization.
  * Equal inputs give equal bits.  Scores, exponentials and sums are fp32; the exponentials are rounded to bf16 for their product with v.
- * Infinities and NaN reach only the queries that attend them; debug checks scan nothing for the calls from here
+ * Infinities and NaN reach only the queries that attend them (one whose scores are all -infinity is 0 / 0: NaN,
+ * with lse = log 0 = -infinity); debug checks scan nothing for the calls from here
  * on, which have no preconditions on device data.  Tq == 0, Hq == 0 or B == 0 is valid and
  * touches nothing; Tk == 0 writes zeros.
  * ------------------------------------------------------------------------------------------- */

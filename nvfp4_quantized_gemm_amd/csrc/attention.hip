@@ -149,16 +149,21 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   total = add_halves(total);
   if (query >= sq.n) return;
   const int64_t row = sq.begin + query;
-  if (a.splits > 1) {  // [splits][Tq][Hq][D] sums relative to 2^top, then [splits][Tq][Hq] (top, sum of weights)
+  // A query without keys gives 0.  One whose scores are all -inf has no weights either, and gives 0 / 0.
+  const bool none = limit < 0;
+  if (a.splits > 1) {  // [splits][Tq][Hq][D] sums relative to 2^top, then [splits][Tq][Hq] (top, sum of weights); top -inf: none
     const int64_t each = (int64_t)a.Tq * a.Hq, at = split * each + row * a.Hq + head;
     store_column_f32<DB>(O, 1.0f, a.parts + at * a.D, a.D, h);
-    if (h == 0) reinterpret_cast<f32x2 *>(a.parts + a.splits * each * a.D)[at] = f32x2{top * scale2, total};
+    if (h == 0) {
+      const float t = none ? -INFINITY : fmaxf(top * scale2, kLowest);
+      reinterpret_cast<f32x2 *>(a.parts + a.splits * each * a.D)[at] = f32x2{t, total};
+    }
     return;
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // a query without keys: 0
+  const float inv = none ? 0.0f : 1.0f / total;
   store_column<DB>(O, inv, static_cast<uint16_t *>(a.out) + row * a.ldo_t + head * a.ldo_h, a.D, h);
   if (a.lse && h == 0)
-    a.lse[(int64_t)head * a.Tq + row] = total == 0.0f ? -INFINITY : (top * scale2 + __builtin_amdgcn_logf(total)) * kLn2;
+    a.lse[(int64_t)head * a.Tq + row] = none ? -INFINITY : (top * scale2 + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 // Joins the splits in order: a thread has 4 values of a query's head.
@@ -179,12 +184,13 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join(const Attention
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] += v[e] * f;
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const bool none = total == 0.0f && top == -INFINITY;
+  const float inv = none ? 0.0f : 1.0f / total;
   const bf16x2 lo = {(__bf16)(o[0] * inv), (__bf16)(o[1] * inv)}, hi = {(__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
   *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + t * a.ldo_t + head * a.ldo_h + d) =
       u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
   if (a.lse && d == 0)
-    a.lse[(int64_t)head * a.Tq + t] = total == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
+    a.lse[(int64_t)head * a.Tq + t] = none ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 constexpr int kWaves = 4;

@@ -17,6 +17,8 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A maximum of scores that are all -inf, where -inf itself says that there is no score.
+constexpr float kLowest = -3.402823466e38f;
 
 // ---- sequences ----------------------------------------------------------------------------------------
 

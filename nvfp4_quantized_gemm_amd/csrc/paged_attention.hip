@@ -228,6 +228,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
       Q[n][s] = __builtin_bit_cast(bf16x8, w);
     }
   const float scale2 = a.scale * kLog2e;
+  bool some = false;  // whether this wave met a token
   float top[NC], total[NC];
   f32x4 O[NC][2 * DB];
 #pragma unroll
@@ -263,6 +264,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
     values.put(tile, pieces);
     load(values, c.v, c.vs, next);
     asm volatile("" ::: "memory");
+    some |= (now.left[0] | now.left[1]) > 0;
     bf16x8 p[NC];
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
@@ -315,7 +317,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
     const int h = 16 * n + col;
     total[n] = add_quarters(total[n]);
     if (g == 0) {
-      tops[wave][h] = top[n];
+      tops[wave][h] = some ? fmaxf(top[n], kLowest) : -INFINITY;
       totals[wave][h] = total[n];
     }
 #pragma unroll
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
     const int head = kv * a.group + first + h;
     const int64_t who = (int64_t)b * a.Hq + head;
     if (a.splits == 1) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = sum == 0.0f && t == -INFINITY ? 0.0f : 1.0f / sum;  // no tokens: 0; scores all -inf: 0 / 0
       const bf16x2 x = {(__bf16)(o[0] * inv), (__bf16)(o[1] * inv)}, y = {(__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
       *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + b * a.ldo_t + head * a.ldo_h + 4 * p) =
           u32x2{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)};
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(256) void k_paged_join(const PagedAttentionArgs a) 
   for (int e = 0; e < 4; ++e) sums[g][p][e] = o[e];
   __syncthreads();
   if (g != 0 || 4 * p >= c.D) return;
-  const float sum = (tops[0] + tops[1]) + (tops[2] + tops[3]), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float sum = (tops[0] + tops[1]) + (tops[2] + tops[3]), inv = sum == 0.0f && top == -INFINITY ? 0.0f : 1.0f / sum;
   float r[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
