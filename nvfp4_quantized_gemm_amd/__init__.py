@@ -867,8 +867,8 @@ def nvfp4_attention_workspace_bytes(Tq: int, Tk: int, Hq: int, Hkv: int, D: int,
 def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False, scale: float | None = None,
                     cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, batch: int = 1,
                     save_lse: bool = False, out=None, lse=None, workspace=None, stream=None):
-    """Softmax attention of q [Tq, Hq, D] over k, v [Tk, Hkv, D] (bf16, token strides from D on and head strides free: views
-    of a QKV output are read in place).  Hq is a multiple of Hkv.  Returns (out, lse): out bf16 [Tq, Hq, D], lse fp32 [Hq, Tq], the
+    """Softmax attention of q [Tq, Hq, D] over k, v [Tk, Hkv, D] (bf16, token strides from D to 2^23 - 1 and head strides free:
+    views of a QKV output are read in place).  Hq is a multiple of Hkv.  Returns (out, lse): out bf16 [Tq, Hq, D], lse fp32 [Hq, Tq], the
     log sums of exponentials that the backward pass reads (None without save_lse or a given lse).
 
     cu_q, cu_k: int32 offsets [sequences + 1] of packed sequences, ascending (the first may be above 0); without them the
@@ -954,10 +954,11 @@ def nvfp4_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
 
 
 def _token_rows_of(t: torch.Tensor) -> torch.Tensor:
-    """_heads_of, and tokens that overlap (a gradient that autograd has expanded over them) copied too."""
+    """_heads_of, and tokens that overlap (a gradient that autograd has expanded over them) or lie 2^23 elements apart or
+    more copied too."""
     t = _heads_of(t)
-    overlap = t.dim() == 3 and t.shape[0] > 1 and t.stride(0) < t.shape[2]
-    return t.clone(memory_format=torch.contiguous_format) if overlap else t
+    taken = t.dim() != 3 or t.shape[0] <= 1 or t.shape[2] <= t.stride(0) < 1 << 23
+    return t if taken else t.clone(memory_format=torch.contiguous_format)
 
 
 class _Attention(torch.autograd.Function):
