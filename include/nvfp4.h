@@ -499,7 +499,9 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
  * q, k, v, sequences, causal and scale, with delta_i = dout_i . o_i, ds_ij = p_ij (dout_i . v_j - delta_i):
  *     dq_i = scale sum_j ds_ij k_j     dv_j = sum_i p_ij dout_i     dk_j = scale sum_i ds_ij q_i
  * dk and dv summed over the query heads that share a key head.  p and ds are rounded to bf16 for these
- * products; the sums are fp32 and run in a fixed order: equal inputs give equal bits.
+ * products; the sums are fp32 and run in a fixed order: equal inputs give equal bits.  p comes from lse, which
+ * fp32 holds to 2^-24 of its value: p is off by about |lse| 2^-23 relative, and gradients of queries whose lse is
+ * beyond 2^16 or so say little (outputs are not formed from lse and hold at any finite score).
  *   dout, out, dq   bf16 [Tq][Hq][D], dk, dv bf16 [Tk][Hkv][D], at their own pitches as above.
  *   dq, dk, dv      written; at no input's address (NVFP4_ERR_STRIDE) and not overlapping any array.  Rows
  *                   of no sequence are left as they were; keys that nothing attends get 0.

@@ -65,7 +65,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   f32x16 O[DB];
 
   // A pass over the keys; the careful one, which keeps infinities and NaN from queries that do not attend
-  // them, only where a masked tile holds some (as a branch inside one loop it took 40 registers from it).
+  // them, only where a masked tile holds some (as a branch inside one loop it took 40 registers from it), or where
+  // a maximum is far.
   auto pass = [&](const bool careful) __attribute__((always_inline)) {
     bool again = false;
     top = -INFINITY;
@@ -106,16 +107,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
       if (__ballot(rise)) {
         const float old = !rise ? 1.0f : top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((top - m) * scale2);
         top = rise ? m : top;
+        if (!careful) again |= rise && fabsf(top * scale2) > kFar;
         total *= old;
 #pragma unroll
         for (int d = 0; d < DB; ++d) O[d] *= old;
       }
       const float shift = top == -INFINITY ? 0.0f : top * scale2;
+      const bool far = careful && fabsf(shift) > kFar;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          S[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i][r], scale2, -shift));
+          S[i][r] = __builtin_amdgcn_exp2f(exponent(S[i][r], scale2, top, shift, far));
           total += S[i][r];
         }
       bool apart = masked && a.causal && tile_nonfinite<P, kKeys>(tv, lane);
@@ -151,13 +154,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int64_t row = sq.begin + query;
   // A query without keys gives 0.  One whose scores are all -inf has no weights either, and gives 0 / 0.
   const bool none = limit < 0;
-  if (a.splits > 1) {  // [splits][Tq][Hq][D] sums relative to 2^top, then [splits][Tq][Hq] (top, sum of weights); top -inf: none
+  if (a.splits > 1) {  // [splits][Tq][Hq][D] sums relative to top, then [splits][Tq][Hq] (top, sum of weights); top -inf: none
     const int64_t each = (int64_t)a.Tq * a.Hq, at = split * each + row * a.Hq + head;
     store_column_f32<DB>(O, 1.0f, a.parts + at * a.D, a.D, h);
-    if (h == 0) {
-      const float t = none ? -INFINITY : fmaxf(top * scale2, kLowest);
-      reinterpret_cast<f32x2 *>(a.parts + a.splits * each * a.D)[at] = f32x2{t, total};
-    }
+    if (h == 0) reinterpret_cast<f32x2 *>(a.parts + a.splits * each * a.D)[at] = f32x2{none ? -INFINITY : fmaxf(top, kLowest), total};
     return;
   }
   const float inv = none ? 0.0f : 1.0f / total;
@@ -173,12 +173,13 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join(const Attention
   if (!holds(joined_rows(a.cu_q, a.B, a.Tq), t)) return;
   const int64_t each = (int64_t)a.Tq * a.Hq;
   const f32x2 *const st = reinterpret_cast<const f32x2 *>(a.parts + a.splits * each * a.D) + r;
+  const float scale2 = a.scale * kLog2e;
   float top = -INFINITY, total = 0.0f;
   for (int s = 0; s < a.splits; ++s) top = fmaxf(top, st[s * each].x);
   f32x4 o = {0, 0, 0, 0};
   for (int s = 0; s < a.splits; ++s) {
     const f32x2 x = st[s * each];
-    const float f = x.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);
+    const float f = x.y == 0.0f ? 0.0f : joined_weight(x.x, top, scale2);
     const f32x4 v = *reinterpret_cast<const f32x4 *>(a.parts + (s * each + r) * a.D + d);
     total += x.y * f;
 #pragma unroll
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join(const Attention
   *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + t * a.ldo_t + head * a.ldo_h + d) =
       u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
   if (a.lse && d == 0)
-    a.lse[(int64_t)head * a.Tq + t] = none ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
+    a.lse[(int64_t)head * a.Tq + t] = none ? -INFINITY : (top * scale2 + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 constexpr int kWaves = 4;

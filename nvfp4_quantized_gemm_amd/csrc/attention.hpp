@@ -19,6 +19,18 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A maximum of scores that are all -inf, where -inf itself says that there is no score.
 constexpr float kLowest = -3.402823466e38f;
+// Exponents are scale2 s - shift in one instruction, with shift the rounded product of scale2 and the maximum: all weights of a
+// query share the factor 2^(what was rounded), which leaves them when they are normed.  From this shift on (where the rounding is
+// 2^-4 at most) they are (s - maximum) scale2, or that factor would leave fp32 from a shift of 2^31 on.
+constexpr float kFar = 1048576.0f;
+__device__ __forceinline__ float exponent(float s, float scale2, float top, float shift, bool far) {
+  return far ? (s - top) * scale2 : __builtin_fmaf(s, scale2, -shift);
+}
+// The weight of sums relative to maximum t beside those relative to top.
+__device__ __forceinline__ float joined_weight(float t, float top, float scale2) {
+  const float a = t * scale2, b = top * scale2;
+  return __builtin_amdgcn_exp2f(fabsf(a) > kFar || fabsf(b) > kFar ? (t - top) * scale2 : a - b);
+}
 
 // ---- sequences ----------------------------------------------------------------------------------------
 

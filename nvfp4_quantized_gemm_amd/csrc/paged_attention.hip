@@ -289,11 +289,23 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
           for (int e = 0; e < 4; ++e) O[n][d][e] *= old;
       }
       const float shift = top[n] == -INFINITY ? 0.0f : top[n] * scale2;
+      const bool far = fabsf(shift) > kFar;
+      if (__builtin_expect(__ballot(far) != 0, 0)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[n][i][e] = exponent(S[n][i][e], scale2, top[n], shift, far);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[n][i][e] = exponent(S[n][i][e], scale2, top[n], shift, false);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(S[n][i][e], scale2, -shift));
+          const float x = __builtin_amdgcn_exp2f(S[n][i][e]);
           total[n] += x;
           p[n][4 * i + e] = (__bf16)x;
         }
