@@ -478,7 +478,8 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
  *                makes a call read or write outside its arrays; where they descend, what the rows between the
  *                least and the largest get is not specified.
  *   scale        finite, > 0 (else NVFP4_ERR_MODE).
- *   out          may be q itself (same pitches), and otherwise must not overlap an input.
+ *   out          may be q itself (same pitches), and otherwise must not overlap an input (at the address of k
+ *                or v: NVFP4_ERR_STRIDE).
  *   lse          NULL, or fp32 [Hq][Tq] (the backward pass reads it).
  *   workspace    nvfp4_attention_workspace_bytes bytes (0 but where there are few queries, whose keys several
  *                workgroups then share, joined in a fixed order), 16-byte aligned, no initialization.
@@ -503,8 +504,8 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
  * fp32 holds to 2^-24 of its value: p is off by about |lse| 2^-23 relative, and gradients of queries whose lse is
  * beyond 2^16 or so say little (outputs are not formed from lse and hold at any finite score).
  *   dout, out, dq   bf16 [Tq][Hq][D], dk, dv bf16 [Tk][Hkv][D], at their own pitches as above.
- *   dq, dk, dv      written; at no input's address (NVFP4_ERR_STRIDE) and not overlapping any array.  Rows
- *                   of no sequence are left as they were; keys that nothing attends get 0.
+ *   dq, dk, dv      written; at no input's and not at each other's address (NVFP4_ERR_STRIDE), and not
+ *                   overlapping any array.  Rows of no sequence are left as they were; keys that nothing attends get 0.
  *   workspace       nvfp4_attention_backward_workspace_bytes bytes, 16-byte aligned, no initialization (where there
  *                   are few queries or keys, several workgroups share a gradient and add it at the end).
  * B == 0 or Hq == 0 is valid and touches nothing; Tq == 0 writes dk = dv = 0. */
@@ -543,7 +544,7 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
  * either one's values may remain.  (T + 15) Hkv (D + 31) / 8 < 2^31.
  *
  * nvfp4_paged_attention: out[b] = softmax(scale q[b] . keys) values over the lengths[b] tokens of sequence b
- * (q, out bf16 [B][Hq][D] at pitches; a sequence without tokens gets 0; out may be q itself with its pitches).  A
+ * (q, out bf16 [B][Hq][D] at pitches; a sequence without tokens gets 0; out may be q itself with its pitches, not the cache).  A
  * sequence's tokens are split over workgroups by its length and joined in a fixed order: equal inputs give
  * equal bits.  workspace: nvfp4_paged_attention_workspace_bytes bytes (0 where nothing is split; capacity =
  * max_pages page_size), 16-byte aligned, no initialization.  Nothing past a sequence's length is read.

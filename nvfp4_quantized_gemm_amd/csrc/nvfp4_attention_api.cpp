@@ -12,7 +12,7 @@ using namespace nvfp4;
 namespace {
 
 constexpr int64_t kMaxCapacity = (int64_t)1 << 30;  // a sequence's positions, and a step past them, fit 32 bits
-constexpr int64_t kMaxPitch = (int64_t)1 << 23;  // offsets inside a tile of 64 rows fit 31 bits
+constexpr int64_t kMaxPitch = (int64_t)1 << 23;  // offsets inside a tile (128 rows at most) fit 31 bits
 
 struct Heads {  // [T][H][D] bf16 at token and head pitches
   const void *p;
@@ -28,6 +28,8 @@ nvfp4_status_t check_heads(const Heads &x, int64_t D, bool written) {
 }
 // the token pitch that the kernels bound their rows by; a single token's is never used, whatever it is
 int64_t row_pitch(const Heads &x, int64_t D) { return x.T > 1 ? x.ld_t : D; }
+// two arrays that begin at one address
+bool same_place(const Heads &a, const Heads &b) { return a.T > 0 && b.T > 0 && a.p == b.p; }
 // a written array at an input's address has its pitches
 bool same_place_fits(const Heads &out, const Heads &in) {
   return out.p != in.p || ((out.T <= 1 || out.ld_t == in.ld_t) && (out.H <= 1 || out.ld_h == in.ld_h));
@@ -100,7 +102,7 @@ nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_hea
   if ((st = check_heads(hq, D, false)) != NVFP4_OK || (st = check_heads(hk, D, false)) != NVFP4_OK ||
       (st = check_heads(hv, D, false)) != NVFP4_OK || (st = check_heads(ho, D, true)) != NVFP4_OK)
     return st;
-  if (!same_place_fits(ho, hq)) return NVFP4_ERR_STRIDE;
+  if (!same_place_fits(ho, hq) || same_place(ho, hk) || same_place(ho, hv)) return NVFP4_ERR_STRIDE;
   const size_t need = nvfp4_attention_workspace_bytes(Tq, Tk, Hq, Hkv, D, B);
   if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (!aligned(lse, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
@@ -140,9 +142,12 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
   for (const Heads &x : grads)
     if ((st = check_heads(x, D, true)) != NVFP4_OK) return st;
   if (Tq > 0 && !lse) return NVFP4_ERR_NULL;
-  for (const Heads &y : grads)
+  for (const Heads &y : grads) {
     for (const Heads &x : in)
       if (y.p && y.T > 0 && y.p == x.p) return NVFP4_ERR_STRIDE;
+    for (const Heads &x : grads)
+      if (&x != &y && same_place(x, y)) return NVFP4_ERR_STRIDE;
+  }
   const size_t need = nvfp4_attention_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, B);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return NVFP4_ERR_WORKSPACE;
@@ -211,7 +216,7 @@ nvfp4_status_t nvfp4_paged_attention(const void *q, int64_t ldq_token, int64_t l
   if (blocks >= (1 << 16)) return NVFP4_ERR_SHAPE;
   const Heads hq{q, B, Hq, ldq_token, ldq_head}, ho{out, B, Hq, ldo_token, ldo_head};
   if ((st = check_heads(hq, D, false)) != NVFP4_OK || (st = check_heads(ho, D, true)) != NVFP4_OK) return st;
-  if (!same_place_fits(ho, hq)) return NVFP4_ERR_STRIDE;
+  if (!same_place_fits(ho, hq) || (pages > 0 && (out == k_cache || out == v_cache))) return NVFP4_ERR_STRIDE;
   const size_t need = nvfp4_paged_attention_workspace_bytes(B, Hq, Hkv, D, max_pages * page_size);
   if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
