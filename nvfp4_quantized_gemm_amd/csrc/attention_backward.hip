@@ -330,15 +330,15 @@ struct GradJoin {
 __global__ __launch_bounds__(kJoinThreads) void k_gradient_join(const GradJoin g) {
   const uint32_t i = blockIdx.x * (uint32_t)kJoinThreads + threadIdx.x, j = blockIdx.y;
   const uint32_t r = fastdiv(i, g.per_row), at = 4 * (i - r * g.per_row.d), t = fastdiv(r, g.heads), head = r - t * g.heads.d;
+  if (!holds(joined_rows(g.cu, g.B, g.T), t)) return;
   const int64_t each = (int64_t)g.T * g.heads.d * g.D;
   const float *from = g.parts + j * each + (int64_t)r * g.D + at;
   f32x4 sum = {0, 0, 0, 0};
-  for (int s = 0; s < (t < (uint32_t)g.T ? g.splits : 0); ++s) {  // on their way while the offsets are looked at
+  for (int s = 0; s < g.splits; ++s) {
     const f32x4 x = *reinterpret_cast<const f32x4 *>(from + gridDim.y * s * each);
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] += x[e];
   }
-  if (!holds(joined_rows(g.cu, g.B, g.T), t)) return;
   const bf16x2 lo = {(__bf16)sum[0], (__bf16)sum[1]}, hi = {(__bf16)sum[2], (__bf16)sum[3]};
   *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(g.out[j]) + t * g.ld_t[j] + head * g.ld_h[j] + at) =
       u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
