@@ -105,7 +105,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
       // Only the queries that need it move theirs, so that a query's bits do not depend on its neighbours.
       const bool rise = (m - top) * scale2 > 8.0f;
       if (__ballot(rise)) {
-        const float old = !rise ? 1.0f : top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((top - m) * scale2);
+        const float old = !rise ? 1.0f : top == -INFINITY ? 0.0f : joined_weight(top, m, scale2);
         top = rise ? m : top;
         if (!careful) again |= rise && fabsf(top * scale2) > kFar;
         total *= old;

@@ -26,7 +26,8 @@ constexpr float kFar = 1048576.0f;
 __device__ __forceinline__ float exponent(float s, float scale2, float top, float shift, bool far) {
   return far ? (s - top) * scale2 : __builtin_fmaf(s, scale2, -shift);
 }
-// The weight of sums relative to maximum t beside those relative to top.
+// The weight of sums relative to maximum t beside those relative to top: by the shifts that they were summed with, whose
+// roundings differ (by the maxima themselves it was off by 2^-5 at shifts of 2^19).
 __device__ __forceinline__ float joined_weight(float t, float top, float scale2) {
   const float a = t * scale2, b = top * scale2;
   return __builtin_amdgcn_exp2f(fabsf(a) > kFar || fabsf(b) > kFar ? (t - top) * scale2 : a - b);

@@ -280,7 +280,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
       m = max_quarters(m);
       const bool rise = (m - top[n]) * scale2 > 8.0f;  // see k_attention
       if (__ballot(rise)) {
-        const float old = !rise ? 1.0f : top[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((top[n] - m) * scale2);
+        const float old = !rise ? 1.0f : top[n] == -INFINITY ? 0.0f : joined_weight(top[n], m, scale2);
         top[n] = rise ? m : top[n];
         total[n] *= old;
 #pragma unroll
@@ -345,7 +345,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC 
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const float l = totals[w][h], f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((tops[w][h] - t) * scale2);
+      const float l = totals[w][h], f = l == 0.0f ? 0.0f : joined_weight(tops[w][h], t, scale2);
       const f32x4 x = *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(smem + w * kPart) + h * kW + 4 * (p ^ (h & 7)));
       sum += l * f;
 #pragma unroll
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(256) void k_paged_join(const PagedAttentionArgs a) 
   if (lane == 0) tops[wave] = top;
   __syncthreads();
   top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((t - top) * scale2);
+  const float f = l == 0.0f ? 0.0f : joined_weight(t, top, scale2);
   weights[threadIdx.x] = f;
   l *= f;
   __syncthreads();
