@@ -483,11 +483,11 @@ nvfp4_status_t nvfp4_rope_axes(const void *x, nvfp4_dtype_t dtype, int64_t T, in
  *   lse          NULL, or fp32 [Hq][Tq] (the backward pass reads it).
  *   workspace    nvfp4_attention_workspace_bytes bytes (0 but where there are few queries, whose keys several
  *                workgroups then share, joined in a fixed order), 16-byte aligned, no initialization.
- * Equal inputs give equal bits.  Scores, exponentials and sums are fp32; the exponentials are rounded to bf16 for their product with v.
+ * Equal inputs give equal bits (a query's bits depend on the others of its call only where keys are shared by
+ * several workgroups: where they are cut depends on the call's sizes).  Scores, exponentials and sums are fp32; the exponentials are rounded to bf16 for their product with v.
  * Infinities and NaN reach only the queries that attend them (one whose scores are all -infinity is 0 / 0: NaN,
- * with lse = log 0 = -infinity); debug checks scan nothing for the calls from here
- * on, which have no preconditions on device data.  Tq == 0, Hq == 0 or B == 0 is valid and
- * touches nothing; Tk == 0 writes zeros.
+ * with lse = log 0 = -infinity).  Debug checks scan nothing for the calls from here on: no device data
+ * makes them leave their arrays.  Tq == 0, Hq == 0 or B == 0 is valid and touches nothing; Tk == 0 writes zeros.
  * ------------------------------------------------------------------------------------------- */
 size_t nvfp4_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, int64_t B);
 nvfp4_status_t nvfp4_attention(const void *q, int64_t ldq_token, int64_t ldq_head, const void *k, int64_t ldk_token,
@@ -532,7 +532,8 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
  *   page_table          device int32 [B][ld_table], max_pages <= ld_table entries of a row used: position p of
  *                       sequence b is row p % page_size of page page_table[b][p / page_size].  An entry
  *                       outside [0, pages) holds no tokens: nothing is read or written there.
- *   lengths             device int32 [B]: tokens of each sequence, taken into [0, max_pages page_size].
+ *   lengths             device int32 [B]: tokens of each sequence (attention takes them into
+ *                       [0, max_pages page_size]; appending leaves out what lies outside).
  *   max_pages page_size < 2^30, B < 2^16, Hq <= 2^16 with Hq a multiple of Hkv.
  * No content of page_table, lengths or cu makes a call read or write outside its arrays.
  *
@@ -540,8 +541,8 @@ nvfp4_status_t nvfp4_attention_backward(const void *dout, int64_t lddo_token, in
  * of new tokens, which `lengths` counts already: with cu NULL token b is the last one of sequence b
  * (T == B), else the tokens cu[b] .. cu[b + 1] - 1 are sequence b's last (device int32 [B + 1], ascending).
  * Tokens past the last sequence, and those whose position is negative or has no page, are not written.  MXFP8 is
- * bit-identical to nvfp4_mx8_quantize's rule.  Two tokens at one place (a page that two sequences write):
- * either one's values may remain.  (T + 15) Hkv (D + 31) / 8 < 2^31.
+ * bit-identical to nvfp4_mx8_quantize's rule.  Two tokens of a call at one place (a page that two sequences
+ * write): values of either one may remain, side by side, and MXFP8 codes of one under scales of the other.  (T + 15) Hkv (D + 31) / 8 < 2^31.
  *
  * nvfp4_paged_attention: out[b] = softmax(scale q[b] . keys) values over the lengths[b] tokens of sequence b
  * (q, out bf16 [B][Hq][D] at pitches; a sequence without tokens gets 0; out may be q itself with its pitches, not the cache).  A

@@ -7,6 +7,10 @@
 // rounded to bf16 where they are and multiply as they lie, O^T += V^T P^T, and the running maximum and sum
 // are one register each.  Keys and values pass through LDS in tiles of 64, two in turn; V^T is read from
 // its rows by the transposing LDS read.
+//
+// Measured: 4096 tokens, 16 heads of 72: 103 us (750 TFLOP/s); 8192 causal, 32 / 8 heads of 128: 528 us (1.04 PFLOP/s).  Bound by
+// issue: the products of one wave of a SIMD hide little of the other's vector instructions (each product costs these about 23
+// of its 32 clocks), so that their times add up: of the prompt's 1.00 M cycles products are 0.53, vector instructions about 0.45.
 #include "attention.hpp"
 
 namespace nvfp4 {
@@ -102,7 +106,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
       for (int r = 0; r < 16; ++r) m = fmaxf(m, S[1][r]);
       m = max_halves(m);
       // The sums are kept relative to a maximum that may lag by 2^8: they cannot overflow, and are as exact.
-      // Only the queries that need it move theirs, so that a query's bits do not depend on its neighbours.
+      // Only the queries that need it move theirs, so that a query's bits do not depend on its neighbours (where workgroups
+      // share keys, they depend on where the keys are cut: on the call's sizes and the block's last query).
       const bool rise = (m - top) * scale2 > 8.0f;
       if (__ballot(rise)) {
         const float old = !rise ? 1.0f : top == -INFINITY ? 0.0f : joined_weight(top, m, scale2);

@@ -73,7 +73,8 @@ __device__ __forceinline__ bool holds(const SeqRows &s, uint32_t row) { return r
 
 // Which block of which head: neighbouring workgroups lie on different XCDs, so where the heads divide evenly
 // each XCD takes its own, and all blocks that read a key head's rows share an L2.  slots_first: block by block
-// over the heads (causal blocks with many tiles go first), else head by head.
+// over the heads, else head by head.  (Causal calls go from the last slot on: of one sequence
+// the blocks with many tiles go first; of several, the last sequence does, whatever its length.)
 __device__ __forceinline__ void block_of(int heads, int slots, bool slots_first, int &head, int &slot) {
   const bool own = heads % 8 == 0;
   const int w = blockIdx.x, per = own ? heads / 8 : heads, i = own ? w >> 3 : w, x = own ? (w & 7) * per : 0;

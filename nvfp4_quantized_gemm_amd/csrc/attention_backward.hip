@@ -8,8 +8,8 @@
 // computing scores and dO V^T twice (seven products instead of five).  P and dS are rounded to bf16 where
 // they are multiplied; everything else is fp32.
 //
-// Measured: 4096 tokens, 16 heads of 72: dQ 144 us, dK and dV 186 us (matrix cores busy 50 and 52 %); 4096 causal, 32 / 8
-// heads of 128: 226 and 312 us (52 and 44 %) and 13 us for the join.  Bound as the forward pass by issue, and at 128 by LDS, of
+// Measured (best of 20): 4096 tokens, 16 heads of 72: dQ 145 us, dK and dV 189 us (matrix cores busy 51 and 52 %); 4096 causal,
+// 32 / 8 heads of 128: 230 and 314 us (51 and 44 %) and 13 us for the join.  Bound as the forward pass by issue, and at 128 by LDS, of
 // which a block of 32 x 32 reads 56 operands of 1 KB for 32 products.
 #include "attention.hpp"
 
@@ -387,7 +387,7 @@ hipError_t launch(AttentionGradArgs g, hipStream_t stream) {
 // Workgroups for two rounds of 256 CUs, but none with less than about 4 steps (4096 causal, 8 key heads of 128: 256 workgroups
 // of very different lengths alone, 512 halves 341 us with the join; 4 key heads of 64, 1600 keys: 49 us alone, 40 shared).
 // Of several sequences the longest is taken for twice the average, it is waited for: queries 129, 64, 1, 500 over 1600 keys, 12 /
-// 4 heads of 64, the whole backward 59 us against 69; eight of 1 and one of 1000 81 and 109; two equal ones of 512 45 and 42.
+// 4 heads of 64, the whole backward 60 us against 69; eight of 1 and one of 1000 81 and 109; two equal ones of 512 45 and 42.
 int attention_backward_splits(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t B) {
   const int64_t blocks = (Tk / (32 * kKeyWaves) + B) * Hkv, want = (512 + blocks - 1) / blocks;
   const int64_t steps = ((B > 1 ? 2 * Tq : Tq) / (B > 0 ? B : 1) / kRows + 1) * (Hq / Hkv), most = steps / 4 > 1 ? steps / 4 : 1;

@@ -92,7 +92,7 @@ __device__ __forceinline__ bf16x8 columns16(const uint8_t *tile, int d, int lane
   return __builtin_bit_cast(bf16x8, s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
 }
 
-// The 8 values of a piece as bf16: codes times their scale (exact, as in the W4A8 product).  The conversion reads the
+// The 8 values of a piece as bf16: codes times their scale (exact down to bf16's least number, 2^-133).  The conversion reads the
 // scale's exponent: 0 stands for 2^-127 (E8M0's least), 255 for NaN.
 __device__ __forceinline__ u32x4 widen_piece(const u32x2 &codes, uint32_t x) {
   const float X = __uint_as_float(x << 23);
@@ -169,8 +169,9 @@ struct TileInFlight {
 // wave takes every fourth 32.  A wave brings a tile from its pages to registers while the one before multiplies, and
 // from there to its own part of LDS (keys first, then values in their place), without barriers; MXFP8 is widened on
 // that way.  Few registers and little LDS, so that 3 waves per SIMD keep loads in flight.
-// Bound by memory in bf16: two sequences of 131072, 8 heads of 128, 134 us (5.5 TB/s; with 32 columns and 2 waves 132); in
-// MXFP8 by issue and LDS beside it: 64 sequences to 8192 116 us (4.8 TB/s; 166 with 32 columns, 130 with 8 bytes a load).
+// Bound by memory in bf16: two sequences of 131072, 8 heads of 128, 134 us (5.5 of the 6.1 TB/s that a large reduction reads;
+// with 32 columns and 2 waves 132); in MXFP8 by issue and LDS beside it: 64 sequences to 8192 119 us (4.7 TB/s; 166 with 32
+// columns, 130 with 8 bytes a load).
 template <int DB, bool MX8, int W, int NC>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NC == 2 ? 2 : 3))) void k_paged_attention(
     const PagedAttentionArgs a) {
